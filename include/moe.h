@@ -298,6 +298,104 @@ MOE_API moe_status moe_layer_forward_noalloc(moe_ctx *ctx, const moe_desc *desc 
                                      const moe_weights *w /* host */, const void *x, int32_t T,
                                      void *out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators next to the layer: RMS norm, the paged KV cache, attention over
+ * it.  They need no moe_ctx; the conventions above hold (device pointers,
+ * 16-byte alignment, asynchronous, arguments checked first, no allocation,
+ * bit-identical results from run to run).  A call with zero rows is a no-op
+ * that returns MOE_OK. */
+
+#define MOE_NO_QUANT (-1)
+
+/* RMS norm with the residual's addition and an output in 8 bits:
+ *
+ *   s = x + residual                               (fp32; s = x if NULL)
+ *   y = s / sqrt(mean(s^2) + eps) * weight         (fp32, from the unrounded s)
+ *   residual_out = s, y_out = y                    (rounded once to `dtype`)
+ *   q: codes of the unrounded y
+ *
+ * dtype: MOE_F32 or MOE_BF16, for x, residual, weight, residual_out and y.
+ * Row strides are in elements, rows contiguous inside; outputs are
+ * [rows][hidden] contiguous and may be the inputs if those are, too.
+ * q_dtype: MOE_NO_QUANT; MOE_MXFP8 (q E4M3 [rows][hidden], q_scale E8M0
+ * [rows][hidden/32], the rule of moe_mx_quantize; hidden a multiple of 32);
+ * MOE_FP8 (E4M3 of y / fp8_scale, the rule of moe_fp8_quantize).  A NaN
+ * becomes the NaN code and an infinity saturates.  residual_out is NULL
+ * exactly where residual is; y may be NULL with an 8-bit output.  Any
+ * hidden >= 1; x, residual, weight, y and residual_out need only their
+ * element's alignment (16 bytes and strides of whole 16-byte pieces are
+ * faster), q 16 bytes. */
+MOE_API moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual,
+                        int64_t residual_stride, const void *weight, int dtype, int32_t rows,
+                        int32_t hidden, float eps, void *residual_out, void *y, int q_dtype,
+                        float fp8_scale, uint8_t *q, uint8_t *q_scale, void *stream);
+
+/* A paged KV cache (host struct): pools of pages
+ * [num_pages][kv_heads][page_size][head_dim] of keys and values.
+ * dtype MOE_BF16 or MOE_F32: elements; MOE_MXFP8: E4M3 codes, with E8M0
+ * scale bytes [num_pages][kv_heads][page_size][head_dim/32].  page_size: a
+ * power of two up to 65536; head_dim 64, 128 or 256.  Activations are bf16
+ * (fp32 for a MOE_F32 cache). */
+typedef struct moe_kv_cache {
+  void *k, *v;
+  uint8_t *k_scale, *v_scale;    /* MOE_MXFP8 only */
+  int32_t num_pages, page_size, kv_heads, head_dim, dtype;
+} moe_kv_cache;
+
+/* One batch of new tokens (host struct; the arrays are on the device).  The
+ * rows row_offsets[s] .. row_offsets[s+1] - 1 of the activations are the last
+ * tokens of sequence s, whose length is kv_len[s] with them; row r is
+ * position kv_len[s] - row_offsets[s+1] + r, and position p lies in slot
+ * p % page_size of page page_table[s][p / page_size].  Entries that are not a
+ * page (negative, or num_pages and above) hold no token.  max_rows: at least
+ * the largest number of new tokens of one sequence.  The arrays are read when
+ * the calls run, so a captured graph follows lengths that change; whatever
+ * they hold, no access leaves the pools and the activations.
+ * max_pages * page_size + rows stays below 2^31. */
+typedef struct moe_kv_batch {
+  const int32_t *page_table;     /* [seqs][max_pages] */
+  const int32_t *row_offsets;    /* [seqs + 1], ascending */
+  const int32_t *kv_len;         /* [seqs] */
+  int32_t seqs, max_pages, rows, max_rows;
+} moe_kv_batch;
+
+/* Write the new tokens' keys and values ([rows][kv_heads][head_dim]; row and
+ * head strides in elements, multiples of 16 bytes) into their pages,
+ * quantised to MX-fp8 where the cache is (the rule of moe_mx_quantize over
+ * head_dim; a NaN becomes the NaN code).  Rows of no sequence or page are
+ * dropped.  moe_kv_read is the way back: k, v [rows][kv_heads][head_dim]
+ * contiguous, dequantised and rounded once; zeros for rows of no sequence or
+ * page. */
+MOE_API moe_status moe_kv_write(const moe_kv_cache *cache /* host */, const moe_kv_batch *batch /* host */,
+                        const void *k, int64_t k_row, int64_t k_head, const void *v,
+                        int64_t v_row, int64_t v_head, void *stream);
+MOE_API moe_status moe_kv_read(const moe_kv_cache *cache /* host */, const moe_kv_batch *batch /* host */,
+                       void *k, void *v, void *stream);
+
+/* Attention of the batch's rows over their sequences in the cache (the new
+ * tokens' keys and values written before):
+ *
+ *   out[r, h] = sum_j softmax_j(scale q[r, h] . k[j, g(h)]) v[j, g(h)],
+ *   g(h) = h / (heads / kv_heads),
+ *
+ * over the keys j <= pos(r); with window > 0 also j > pos(r) - window or
+ * j < sinks.  A row that sees no key (or belongs to no sequence) gives zeros;
+ * what masked slots hold, NaN included, does not reach a row whose whole
+ * sequence masks them.  q: [rows][heads][head_dim], row and head strides in
+ * elements, multiples of 16 bytes; out: [rows][heads][head_dim] contiguous.
+ * Products of bf16 operands (MX-fp8 keys and values are exact in bf16) or
+ * fp32 ones, accumulated in fp32; softmax statistics in fp32; with a bf16 or
+ * MX-fp8 cache the softmax weights are rounded to bf16 before they multiply
+ * the values.  ws: moe_attention_workspace_bytes() bytes (0 is returned for
+ * invalid arguments), its contents need not outlive the call's kernels. */
+MOE_API size_t moe_attention_workspace_bytes(const moe_kv_cache *cache /* host */,
+                                     const moe_kv_batch *batch /* host */, int32_t heads,
+                                     int32_t window, int32_t sinks);
+MOE_API moe_status moe_attention(const moe_kv_cache *cache /* host */, const moe_kv_batch *batch /* host */,
+                         const void *q, int64_t q_row, int64_t q_head, int32_t heads, float scale,
+                         int32_t window, int32_t sinks, void *out, void *ws, size_t ws_bytes,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,4 +5,4 @@ gfx950, built from ``csrc/``); :mod:`.binding` is a thin ctypes layer over it.
 The library is loaded on first use and loading fails loudly if it has not
 been built: there is no fallback path.
 """
-__all__ = ["binding", "inputs"]
+__all__ = ["binding", "block", "inputs"]

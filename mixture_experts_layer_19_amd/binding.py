@@ -25,7 +25,10 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_status_string", "moe_ctx_la
            "moe_fp8_quantize",
            "moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_ws_topk", "moe_ctx_set_profiling", "moe_ctx_stage_ms",
-           "moe_layer_forward_noalloc")
+           "moe_layer_forward_noalloc",
+           "moe_rms_norm", "moe_kv_write", "moe_kv_read", "moe_attention_workspace_bytes",
+           "moe_attention")
+MOE_NO_QUANT = -1
 STAGES = ("route", "mx_quant", "permute", "gate_up", "down", "shared_gate_up", "shared_down",
           "combine")
 
@@ -44,6 +47,20 @@ class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "router_w", "router_bias", "gate_up", "down", "gate_up_scale", "down_scale",
         "sh_gate_up", "sh_down", "sh_gate_up_scale", "sh_down_scale")]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class MoeKvBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -86,6 +103,13 @@ def lib():
             "moe_layer_ws_topk": ([DP, I32, ctypes.POINTER(S), ctypes.POINTER(S)], ctypes.c_int),
             "moe_ctx_set_profiling": ([P, ctypes.c_int], ctypes.c_int),
             "moe_ctx_stage_ms": ([P, ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
+            "moe_rms_norm": ([P, I64, P, I64, P, ctypes.c_int, I32, I32, ctypes.c_float, P, P,
+                              ctypes.c_int, ctypes.c_float, P, P, P], ctypes.c_int),
+            "moe_kv_write": ([P, P, P, I64, I64, P, I64, I64, P], ctypes.c_int),
+            "moe_kv_read": ([P, P, P, P, P], ctypes.c_int),
+            "moe_attention_workspace_bytes": ([P, P, I32, I32, I32], S),
+            "moe_attention": ([P, P, P, I64, I64, I32, ctypes.c_float, I32, I32, P, P, S, P],
+                              ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -216,3 +240,34 @@ def moe_ctx_stage_ms(ctx) -> dict:
     arr = (ctypes.c_float * len(STAGES))()
     _check(lib().moe_ctx_stage_ms(ctx, arr), ctx)
     return dict(zip(STAGES, (float(v) for v in arr)))
+
+
+def moe_rms_norm(x, x_stride, residual, residual_stride, weight, dtype, rows, hidden, eps,
+                 residual_out, y, q_dtype, fp8_scale, q, q_scale, stream=None):
+    _check(lib().moe_rms_norm(_ptr(x), x_stride, _ptr(residual), residual_stride, _ptr(weight),
+                              dtype, rows, hidden, eps, _ptr(residual_out), _ptr(y), q_dtype,
+                              fp8_scale, _ptr(q), _ptr(q_scale), _stream(stream)))
+
+
+def moe_kv_write(cache: MoeKvCache, batch: MoeKvBatch, k, k_row, k_head, v, v_row, v_head,
+                 stream=None):
+    _check(lib().moe_kv_write(ctypes.byref(cache), ctypes.byref(batch), _ptr(k), k_row, k_head,
+                              _ptr(v), v_row, v_head, _stream(stream)))
+
+
+def moe_kv_read(cache: MoeKvCache, batch: MoeKvBatch, k, v, stream=None):
+    _check(lib().moe_kv_read(ctypes.byref(cache), ctypes.byref(batch), _ptr(k), _ptr(v),
+                             _stream(stream)))
+
+
+def moe_attention_workspace_bytes(cache: MoeKvCache, batch: MoeKvBatch, heads: int, window: int,
+                                  sinks: int) -> int:
+    return lib().moe_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(batch), heads,
+                                               window, sinks)
+
+
+def moe_attention(cache: MoeKvCache, batch: MoeKvBatch, q, q_row, q_head, heads, scale, window,
+                  sinks, out, ws, ws_bytes, stream=None):
+    _check(lib().moe_attention(ctypes.byref(cache), ctypes.byref(batch), _ptr(q), q_row, q_head,
+                               heads, scale, window, sinks, _ptr(out), _ptr(ws), ws_bytes,
+                               _stream(stream)))

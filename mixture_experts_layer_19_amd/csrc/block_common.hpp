@@ -1,0 +1,104 @@
+// block_common.hpp -- device helpers shared by the norm, cache and attention
+// kernels.
+#pragma once
+#include "block_launch.hpp"
+#include "moe_common.hpp"
+
+namespace moe {
+
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
+
+constexpr float kNegBig = -1e30f;     // running maximum before any key: finite, below every score
+
+// v, its magnitude limited to 448; a NaN stays one.
+__device__ __forceinline__ float e4m3_clamp(float v) {
+  return fabsf(v) > 448.0f ? copysignf(448.0f, v) : v;
+}
+// E4M3 codes of four values, round to nearest even, saturating, NaN kept (the
+// conversion instruction itself turns values above 464 into NaN).
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_clamp(a), e4m3_clamp(b), 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_clamp(c), e4m3_clamp(d), w, true);
+  return (uint32_t)w;
+}
+// Two bf16 (packed) of two fp32 values, round to nearest even, NaN kept.
+__device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+// Four bf16 of four E4M3 codes times the power of two with E8M0 byte `sb`.
+// The instruction takes the exponent field of its scale operand, so byte 0 is
+// 2^-127 and byte 255 NaN; every product is exact in bf16.
+__device__ __forceinline__ uint2 e4m3_to_bf16x4(uint32_t codes, uint32_t sb) {
+  const float s = __uint_as_float(sb << 23);
+  return make_uint2(
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true)));
+}
+
+// Largest / sum over the two half waves and over the four rows of 16 lanes.
+__device__ __forceinline__ float max_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_rows16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max_half(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_rows16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return sum_half(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// ----------------------------------------------------------------------------- batch geometry
+
+// One sequence of a batch.  Whatever the device arrays hold, rows stay inside
+// [0, rows) and keys inside the table's capacity.
+struct SeqGeo {
+  int r0, n;       // first row and number of new rows
+  int pos0;        // position of the first new token (negative: before the sequence)
+  int len;         // tokens that the table can hold of kv_len
+};
+__device__ __forceinline__ SeqGeo seq_geo(const KvArgs &c, int s) {
+  SeqGeo g;
+  const int o0 = c.offsets[s], o1 = c.offsets[s + 1], kvl = max(c.kv_len[s], 0);
+  g.r0 = min(max(o0, 0), c.rows);
+  g.n = min(max(o1, g.r0), c.rows) - g.r0;
+  g.pos0 = kvl - g.n;
+  const long long cap = (long long)c.max_pages << c.page_shift;
+  g.len = (int)min((long long)kvl, cap);
+  return g;
+}
+
+// Sequence of row r (every lane of the wave asks for the same r): the last
+// one that starts at or before it; -1 where no sequence holds the row.
+__device__ __forceinline__ int seq_of_row(const KvArgs &c, int r) {
+  const int lane = threadIdx.x & 63;
+  int below = 0;
+  for (int s0 = 0; s0 <= c.seqs; s0 += 64) {
+    const int s = s0 + lane;
+    const unsigned long long m = __ballot(s <= c.seqs && c.offsets[min(s, c.seqs)] <= r);
+    below += __popcll(m);
+    if (m != ~0ull) break;
+  }
+  const int s = below - 1;
+  return s >= 0 && s < c.seqs ? s : -1;
+}
+
+// Index of a key's row in the pool, ((page * kv_heads + head) * page_size +
+// slot), or -1 where the table holds no page for it.
+__device__ __forceinline__ long long pool_row(const KvArgs &c, int page, int head, int key) {
+  if ((unsigned)page >= (unsigned)c.num_pages) return -1;
+  return ((((long long)page * c.kv_heads + head) << c.page_shift) |
+          (key & ((1 << c.page_shift) - 1)));
+}
+
+}  // namespace moe

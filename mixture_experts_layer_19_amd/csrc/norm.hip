@@ -1,0 +1,260 @@
+// norm.hip -- RMS norm with the residual's addition and an output in 8 bits.
+//
+//   s = x + residual                      (fp32)
+//   y = s / sqrt(mean(s^2) + eps) * weight
+//   residual_out = round(s), y_out = round(y)
+//   q = E4M3 codes of y: under one E8M0 scale per 32 (MX) or of y / fp8_scale
+//
+// Every output is rounded once, from fp32: the norm takes the unrounded sum
+// and the codes the unrounded y.
+//
+// Bound by memory: a bf16 row with MX output moves 9.03 bytes an element.
+// One pass: a row stays in registers between the sum of squares and its use,
+// in one wave up to 2048 elements (no LDS, no barrier) and in a workgroup of
+// 256 up to 8192; longer rows, rows that are not 16-byte aligned and odd
+// lengths are read a second time (norm_loop_kernel).
+#include "block_common.hpp"
+
+namespace moe {
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, long long i, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint4 u = *(const uint4 *)((const uint16_t *)p + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = *(const float4 *)((const float *)p + i);
+    const float4 b = *(const float4 *)((const float *)p + i + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, long long i, const float (&v)[8]) {
+  if constexpr (BF16) {
+    *(uint4 *)((uint16_t *)p + i) = make_uint4(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]),
+                                               bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7]));
+  } else {
+    *(float4 *)((float *)p + i) = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4 *)((float *)p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+// n of 8 elements, one at a time
+template <bool BF16>
+__device__ __forceinline__ void load_n(const void *p, long long i, int n, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.0f;
+    if (j < n) {
+      if constexpr (BF16) v[j] = bf16_to_f32(((const uint16_t *)p)[i + j]);
+      else v[j] = ((const float *)p)[i + j];
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_n(void *p, long long i, int n, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) {
+      if constexpr (BF16) ((uint16_t *)p)[i + j] = (uint16_t)bf16_pack2(v[j], 0.0f);
+      else ((float *)p)[i + j] = v[j];
+    }
+}
+
+// 8-bit output of 8 consecutive elements (n of them present; MX: all, four
+// neighbouring lanes hold one block of 32 and take its maximum together).
+template <int Q>
+__device__ __forceinline__ void store_codes(const NormArgs &a, long long i, int n, bool whole,
+                                            const float (&y)[8]) {
+  if constexpr (Q == FMT_MX8) {
+    float am = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(y[j]));
+    am = fmaxf(am, __shfl_xor(am, 1, 64));
+    am = fmaxf(am, __shfl_xor(am, 2, 64));
+    const uint32_t sb = mx_scale_byte(am);
+    const float inv = mx_inv_scale(sb);
+    const uint2 w = make_uint2(e4m3_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               e4m3_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+    if (n > 0) {
+      *(uint2 *)(a.q + i) = w;
+      if ((threadIdx.x & 3) == 0) a.q_scale[i >> 5] = (uint8_t)sb;
+    }
+  } else if constexpr (Q == FMT_FP8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = y[j] / a.fp8_scale;
+    const uint2 w = make_uint2(e4m3_pack4(v[0], v[1], v[2], v[3]),
+                               e4m3_pack4(v[4], v[5], v[6], v[7]));
+    if (whole) {
+      *(uint2 *)(a.q + i) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) a.q[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    }
+  }
+}
+
+// Sum over LANES threads: a wave, or a workgroup of 256.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+#pragma unroll
+  for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m, 64);
+  v = sum_rows16(v);
+  if constexpr (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0] + red[1] + red[2] + red[3];
+  }
+  return v;
+}
+
+// A row per LANES threads, NV runs of 8 elements a thread, in registers.
+template <bool BF16, int Q, int LANES, int NV>
+__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
+  __shared__ float red[4];
+  const int lane = threadIdx.x % LANES;
+  const int row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  if (LANES <= 64 && row >= a.rows) return;
+  const int nvec = a.hidden / 8;
+  float v[NV][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = lane + i * LANES;
+    if (c < nvec) {
+      load8<BF16>(a.x, row * a.x_stride + 8 * c, v[i]);
+      if (a.residual) {
+        float r[8];
+        load8<BF16>(a.residual, row * a.residual_stride + 8 * c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  }
+  const float rs = 1.0f / sqrtf(row_sum<LANES>(ss, red) / (float)a.hidden + a.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = lane + i * LANES;
+    const bool in = c < nvec;
+    const long long at = (long long)row * a.hidden + 8 * c;
+    float y[8];
+    if (in) {
+      if (a.residual_out) store8<BF16>(a.residual_out, at, v[i]);
+      float w[8];
+      load8<BF16>(a.weight, 8 * c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rs * w[j];
+      if (a.y) store8<BF16>(a.y, at, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+    }
+    store_codes<Q>(a, at, in ? 8 : 0, in, y);
+  }
+}
+
+// Any length and alignment: a workgroup per row, the row read twice.
+// Everything is written in the second pass, so outputs may be the inputs.
+template <bool BF16, int Q, bool VEC>
+__global__ __launch_bounds__(256) void norm_loop_kernel(NormArgs a) {
+  __shared__ float red[4];
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int nvec = (a.hidden + 7) / 8;
+  auto load = [&](int c, float (&v)[8]) {
+    const int n = min(8, a.hidden - 8 * c);
+    float r[8];
+    if constexpr (VEC) load8<BF16>(a.x, row * a.x_stride + 8 * c, v);
+    else load_n<BF16>(a.x, row * a.x_stride + 8 * c, n, v);
+    if (a.residual) {
+      if constexpr (VEC) load8<BF16>(a.residual, row * a.residual_stride + 8 * c, r);
+      else load_n<BF16>(a.residual, row * a.residual_stride + 8 * c, n, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
+    }
+    return n;
+  };
+  float ss = 0.0f;
+  for (int c = tid; c < nvec; c += 256) {
+    float v[8];
+    load(c, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+  }
+  const float rs = 1.0f / sqrtf(row_sum<256>(ss, red) / (float)a.hidden + a.eps);
+  for (int c0 = 0; c0 < nvec; c0 += 256) {       // every lane takes part in the block maxima
+    const int c = c0 + tid;
+    const long long at = (long long)row * a.hidden + 8 * c;
+    float y[8];
+    int n = 0;
+    if (c < nvec) {
+      float v[8], w[8];
+      n = load(c, v);
+      if constexpr (VEC) {
+        load8<BF16>(a.weight, 8 * c, w);
+        if (a.residual_out) store8<BF16>(a.residual_out, at, v);
+      } else {
+        load_n<BF16>(a.weight, 8 * c, n, w);
+        if (a.residual_out) store_n<BF16>(a.residual_out, at, n, v);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = v[j] * rs * w[j];
+      if (a.y) {
+        if constexpr (VEC) store8<BF16>(a.y, at, y);
+        else store_n<BF16>(a.y, at, n, y);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+    }
+    store_codes<Q>(a, at, n, VEC && n > 0, y);
+  }
+}
+
+namespace {
+bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+template <bool BF16, int Q>
+void launch(const NormArgs &a, hipStream_t s) {
+  const long long e = BF16 ? 8 : 4;              // elements of 16 bytes
+  const bool vec = a.hidden % 8 == 0 && a.x_stride % e == 0 && a.residual_stride % e == 0 &&
+                   al16(a.x) && al16(a.residual) && al16(a.weight) && al16(a.residual_out) &&
+                   al16(a.y);
+  const int nvec = a.hidden / 8;
+  const dim3 g1((a.rows + 3) / 4), g4(a.rows);
+  if (!vec) norm_loop_kernel<BF16, Q, false><<<g4, 256, 0, s>>>(a);
+  else if (nvec <= 64) norm_kernel<BF16, Q, 64, 1><<<g1, 256, 0, s>>>(a);
+  else if (nvec <= 128) norm_kernel<BF16, Q, 64, 2><<<g1, 256, 0, s>>>(a);
+  else if (nvec <= 256) norm_kernel<BF16, Q, 64, 4><<<g1, 256, 0, s>>>(a);
+  else if (nvec <= 512) norm_kernel<BF16, Q, 256, 2><<<g4, 256, 0, s>>>(a);
+  else if (nvec <= 1024) norm_kernel<BF16, Q, 256, 4><<<g4, 256, 0, s>>>(a);
+  else norm_loop_kernel<BF16, Q, true><<<g4, 256, 0, s>>>(a);
+}
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs &a, int is_bf16, int q_fmt, hipStream_t s) {
+  if (a.rows <= 0) return hipSuccess;
+  if (is_bf16) {
+    if (q_fmt == FMT_MX8) launch<true, FMT_MX8>(a, s);
+    else if (q_fmt == FMT_FP8) launch<true, FMT_FP8>(a, s);
+    else launch<true, -1>(a, s);
+  } else {
+    if (q_fmt == FMT_MX8) launch<false, FMT_MX8>(a, s);
+    else if (q_fmt == FMT_FP8) launch<false, FMT_FP8>(a, s);
+    else launch<false, -1>(a, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe
