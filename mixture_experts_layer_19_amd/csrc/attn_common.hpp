@@ -45,4 +45,57 @@ struct RowMask {
   __device__ __forceinline__ bool sees(int key) const { return key < hi && (key >= lo || key < sinks); }
 };
 
+// Values that are not finite.  The second product multiplies every key of a
+// tile, also with the zero weights of rows that do not see it; so in tiles
+// that some rows see partly, elements that are not finite are zero in LDS and
+// are added afterwards, by add_not_finite, to the rows that do see them.
+//
+// Whether a 32-bit word of a pool holds one (MX: a NaN code).
+template <int F>
+__device__ __forceinline__ bool word_not_finite(uint32_t w) {
+  if constexpr (F == FMT_MX8) return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  else if constexpr (F == FMT_BF16) return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+  else return (w & 0x7F800000u) == 0x7F800000u;
+}
+// E8M0 byte from which an E4M3 value may be infinite in bf16 (255: is NaN)
+constexpr uint32_t kScaleOverflow = 247;
+// A word of LDS (two bf16, or one fp32) with zeros in their place.
+template <int F>
+__device__ __forceinline__ uint32_t word_finite(uint32_t w) {
+  if constexpr (F == FMT_F32) return (w & 0x7F800000u) == 0x7F800000u ? 0u : w;
+  const uint32_t lo = (w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu;
+  return lo | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+}
+// What is not finite of elements [d, d + 4) of pool row r, zero elsewhere.
+template <int F, int HD>
+__device__ __forceinline__ f32x4 not_finite4(const KvArgs &c, long long r, int d) {
+  const long long at = r * HD + d;
+  f32x4 v;
+  if constexpr (F == FMT_F32) {
+    v = *(const f32x4 *)(c.v + 4 * at);
+  } else {
+    uint2 w;
+    if constexpr (F == FMT_BF16) w = *(const uint2 *)(c.v + 2 * at);
+    else w = e4m3_to_bf16x4(*(const uint32_t *)(c.v + at), c.v_scale[at >> 5]);
+    v = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+              __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = word_not_finite<FMT_F32>(__float_as_uint(v[i])) ? v[i] : 0.0f;
+  return v;
+}
+
+// Zeros for the rows before the first and past the last sequence.
+template <int F, int HD>
+__device__ __forceinline__ void clear_free_rows(const AttnArgs &a) {
+  const KvArgs &c = a.c;
+  const int first = min(max(c.offsets[0], 0), c.rows), last = min(max(c.offsets[c.seqs], 0), c.rows);
+  if (first == 0 && last == c.rows) return;
+  const long long per_row = (long long)a.heads * HD * (F == FMT_F32 ? 4 : 2) / 16;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < c.rows * per_row; i += gridDim.x * 256ll) {
+    const long long r = i / per_row;
+    if (r < first || r >= last) ((uint4 *)a.out)[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 }  // namespace moe

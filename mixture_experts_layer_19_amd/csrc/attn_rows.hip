@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int p = 0; p < R::q_pieces; ++p) {
         const int off = F == FMT_MX8 ? HD / 2 * g4 + 16 * p : 64 * p + 16 * g4;
-        q[rt][p] = in ? *(const i32x4 *)(qp + off) : i32x4{0, 0, 0, 0};
+        q[rt][p] = in ? *(const i32x4 *)(qp + off) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
       }
       const RowMask mask(g, tok, in, a.window, a.sinks);
       hi[rt] = mask.hi;
@@ -212,21 +212,27 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     };
 
     // V into this wave's LDS: [key][head_dim], bf16 or fp32
-    auto store_v = [&](const i32x4 (&d)[NKH][R::pieces], const uint32_t (&sb)[NKH][R::scales]) MOE_INLINE {
+    // (`finite`: zeros in place of what is not)
+    auto store_v = [&](auto finite) MOE_INLINE {
+      auto put = [&](uint8_t *to, uint4 w) MOE_INLINE {
+        if constexpr (finite)
+          w = make_uint4(word_finite<F>(w.x), word_finite<F>(w.y), word_finite<F>(w.z), word_finite<F>(w.w));
+        *(uint4 *)to = w;
+      };
       static_for<NKH>([&](auto kh) MOE_INLINE {
         uint8_t *dst = own + (16 * kh + l16) * R::v_pitch;
         static_for<R::pieces>([&](auto p) MOE_INLINE {
           if constexpr (F == FMT_MX8) {
             constexpr int si = R::scales == 1 ? 0 : p / 2;
-            uint4 *to = (uint4 *)(dst + HD / 2 * g4 + 32 * p);
-            const uint2 w0 = e4m3_to_bf16x4(d[kh][p][0], sb[kh][si]);
-            const uint2 w1 = e4m3_to_bf16x4(d[kh][p][1], sb[kh][si]);
-            const uint2 w2 = e4m3_to_bf16x4(d[kh][p][2], sb[kh][si]);
-            const uint2 w3 = e4m3_to_bf16x4(d[kh][p][3], sb[kh][si]);
-            to[0] = make_uint4(w0.x, w0.y, w1.x, w1.y);
-            to[1] = make_uint4(w2.x, w2.y, w3.x, w3.y);
+            uint8_t *to = dst + HD / 2 * g4 + 32 * p;
+            const uint2 w0 = e4m3_to_bf16x4(vr[kh][p][0], vs[kh][si]);
+            const uint2 w1 = e4m3_to_bf16x4(vr[kh][p][1], vs[kh][si]);
+            const uint2 w2 = e4m3_to_bf16x4(vr[kh][p][2], vs[kh][si]);
+            const uint2 w3 = e4m3_to_bf16x4(vr[kh][p][3], vs[kh][si]);
+            put(to, make_uint4(w0.x, w0.y, w1.x, w1.y));
+            put(to + 16, make_uint4(w2.x, w2.y, w3.x, w3.y));
           } else {
-            *(i32x4 *)(dst + 64 * p + 16 * g4) = d[kh][p];
+            put(dst + 64 * p + 16 * g4, __builtin_bit_cast(uint4, vr[kh][p]));
           }
         });
       });
@@ -238,7 +244,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     };
     f32x4 sc[RT][NKH];
     // O^T += V^T P^T, the weights in sc
-    auto add_pv = [&](f32x4 (&acc)[RT][DT]) MOE_INLINE {
+    auto add_pv = [&]() MOE_INLINE {
       if constexpr (F == FMT_F32) {
         static_for<NKH>([&](auto kh) MOE_INLINE {
 #pragma unroll
@@ -249,7 +255,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
               const float v = vp[16 * d];
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt)
-                acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, sc[rt][kh][i], acc[rt][d], 0, 0, 0);
+                o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, sc[rt][kh][i], o[rt][d], 0, 0, 0);
             }
           }
         });
@@ -273,15 +279,24 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
             const auto v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-              acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, pw[rt]), acc[rt][d], 0, 0, 0);
+              o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, pw[rt]), o[rt][d], 0, 0, 0);
           }
         });
       }
     };
-    auto next_v = [&](int t) MOE_INLINE {
-      load_rows(c.v, c.v_scale, vr, vs);
-      if (t + 2 < t1) load_pages(t + 2);
+    auto add_not_finite = [&](int k0) MOE_INLINE {
+      for (int key = k0; key < k0 + C::keys && key < g.len; ++key) {
+        const long long r = pool_row(c, pages[key >> c.page_shift], h, key);
+        if (r < 0) continue;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const f32x4 v = not_finite4<F, HD>(c, r, 16 * d + 4 * g4);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            if (key < hi[rt] && (key >= lo[rt] || key < a.sinks)) o[rt][d] += v;
+        }
+      }
     };
     auto clear_v = [&](i32x4 (&d)[R::pieces], uint32_t (&sb)[R::scales]) MOE_INLINE {
 #pragma unroll
@@ -296,16 +311,11 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int p = 0; p < R::pieces; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = (uint32_t)d[p][i];
-          if constexpr (F == FMT_MX8) bad = bad || (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u);
-          else if constexpr (F == FMT_BF16)
-            bad = bad || (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-          else bad = bad || (w & 0x7F800000u) == 0x7F800000u;
-        }
+        for (int i = 0; i < 4; ++i)
+          bad = bad || word_not_finite<F>((uint32_t)d[p][i]);
       if constexpr (F == FMT_MX8)
 #pragma unroll
-        for (int i = 0; i < R::scales; ++i) bad = bad || sb[i] >= 246;
+        for (int i = 0; i < R::scales; ++i) bad = bad || sb[i] >= kScaleOverflow;
       return bad;
     };
     // tokens of the row tile
@@ -407,49 +417,22 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
         static_for<NKH>([&](auto kh) MOE_INLINE {
           if (row[kh] < 0) clear_v(vr[kh], vs[kh]);
         });
-      // A key that some rows of the tile see and others do not: its weight is
-      // zero for those others, which holds only if its value is finite.
+      // keys that some rows of the tile see and others do not
       bool unsafe = false;
       if (tok_b > tok_a && (k0 + C::keys > g.pos0 + tok_a + 1 || (a.window && k0 <= g.pos0 + tok_b - a.window)))
         static_for<NKH>([&](auto kh) MOE_INLINE { unsafe = unsafe || not_finite(vr[kh], vs[kh]); });
-      if (!__ballot(unsafe)) {
-        store_v(vr, vs);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) next_v(t);
-        wave_sync();
-        add_pv(o);
-        wave_sync();
-      } else {
-        // One token at a time, the keys it does not see cleared; a lane keeps the
-        // result of its own row's token.
-        for (int tok = tok_a; tok <= tok_b; ++tok) {
-          const RowMask mask(g, tok, true, a.window, a.sinks);
-          i32x4 vt[NKH][R::pieces];
-          uint32_t st[NKH][R::scales];
-          static_for<NKH>([&](auto kh) MOE_INLINE {
-#pragma unroll
-            for (int i = 0; i < R::pieces; ++i) vt[kh][i] = vr[kh][i];
-#pragma unroll
-            for (int i = 0; i < R::scales; ++i) st[kh][i] = vs[kh][i];
-            if (!mask.sees(k0 + 16 * kh + l16)) clear_v(vt[kh], st[kh]);
-          });
-          store_v(vt, st);
-          wave_sync();
-          f32x4 tmp[RT][DT];
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int d = 0; d < DT; ++d) tmp[rt][d] = o[rt][d];
-          add_pv(tmp);
-          wave_sync();
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-              if ((rt0 + 16 * rt + l16) / a.group == tok) o[rt][d] = tmp[rt][d];
-        }
-        if (more) next_v(t);
+      const bool fix = __ballot(unsafe) != 0;
+      if (fix) store_v(std::true_type{});
+      else store_v(std::false_type{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) {
+        load_rows(c.v, c.v_scale, vr, vs);
+        if (t + 2 < t1) load_pages(t + 2);
       }
+      wave_sync();
+      add_pv();
+      if (fix) add_not_finite(k0);
+      wave_sync();
     }
 
     // merge the four waves: O [row][head_dim], maximum and sum of each row
@@ -520,15 +503,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int units) {
   __shared__ float redm[SL][2];
   const KvArgs &c = a.c;
   const int tid = threadIdx.x, col = tid % COLS, sl = tid / COLS;
-  // rows before the first and past the last sequence
-  const int first_row = min(max(c.offsets[0], 0), c.rows), last_row = min(max(c.offsets[c.seqs], 0), c.rows);
-  if (first_row > 0 || last_row < c.rows) {
-    const long long per_row = (long long)a.heads * HD * (F == FMT_F32 ? 4 : 2) / 16;
-    for (long long i = blockIdx.x * 256ll + tid; i < c.rows * per_row; i += gridDim.x * 256ll) {
-      const long long r = i / per_row;
-      if (r < first_row || r >= last_row) ((uint4 *)a.out)[i] = make_uint4(0, 0, 0, 0);
-    }
-  }
+  clear_free_rows<F, HD>(a);
   const int quad = blockIdx.x % QUADS, h = blockIdx.x / QUADS % c.kv_heads;
   const int s = blockIdx.x / QUADS / c.kv_heads / units, rt = blockIdx.x / QUADS / c.kv_heads % units;
   const SeqGeo g = seq_geo(c, s);
@@ -635,14 +610,10 @@ auto pick(const KvArgs &c, int group, Fn &&f) {
 }
 }  // namespace
 
-size_t attn_ws_bytes(const KvArgs &c, int heads, int window, int sinks) {
-  if (c.rows <= 0) return 0;
-  const int group = heads / c.kv_heads;
-  return pick(c, group, [&](auto l) { return l.ws(c, group); });
+size_t attn_rows_ws_bytes(const AttnArgs &a) {
+  return pick(a.c, a.group, [&](auto l) { return l.ws(a.c, a.group); });
 }
-
-hipError_t launch_attention(const AttnArgs &a, hipStream_t s) {
-  if (a.c.rows <= 0) return hipSuccess;
+hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t s) {
   return pick(a.c, a.group, [&](auto l) { return l.run(a, s); });
 }
 

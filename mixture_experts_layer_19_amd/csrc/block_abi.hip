@@ -1,5 +1,7 @@
 // block_abi.hip -- the C ABI of the operators next to the MoE layer (declared
 // in include/moe.h): argument checks, then the launches.
+#include <math.h>
+
 #include "../../include/moe.h"
 #include "block_common.hpp"
 
@@ -79,6 +81,15 @@ moe_status attn_args(const moe_kv_cache *cache, const moe_kv_batch *batch, int h
   return MOE_OK;
 }
 
+// Which kernel: up to 32 rows (tokens x heads of a group) a sequence fit the
+// row kernel's tile, which reads the keys once and is bound by that.
+bool few_rows(const AttnArgs &a) { return (long long)a.c.max_rows * a.group <= 32; }
+
+size_t workspace(const AttnArgs &a) {
+  if (a.c.rows <= 0) return 0;
+  return few_rows(a) ? attn_rows_ws_bytes(a) : attn_tile_ws_bytes(a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,7 +141,7 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache *cache, const moe_kv_bat
                                      int32_t heads, int32_t window, int32_t sinks) {
   AttnArgs a;
   if (attn_args(cache, batch, heads, window, sinks, &a) != MOE_OK) return 0;
-  return attn_ws_bytes(a.c, a.heads, a.window, a.sinks);
+  return workspace(a);
 }
 
 moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, const void *q,
@@ -143,16 +154,20 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   if (a.c.rows == 0) return MOE_OK;
   if (!q || !out || !al(q, 16) || !al(out, 16) || !al(ws, 16) || !strides_ok(a.c, q_row, q_head))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = attn_ws_bytes(a.c, a.heads, a.window, a.sinks);
+  const size_t need = workspace(a);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   a.q = q;
   a.q_row = q_row;
   a.q_head = q_head;
-  a.scale = scale * 1.44269504088896340736f;
+  // the kernels take maxima of unscaled scores, so the scale's sign goes into q;
+  // a zero scale becomes one that no product of finite scores notices
+  a.q_sign = scale < 0.0f ? (a.c.fmt == FMT_F32 ? 0x80000000u : 0x80008000u) : 0u;
+  a.scale = fmaxf(fabsf(scale) * 1.44269504088896340736f, 1.2e-38f);
   a.out = out;
   a.part = (float *)ws;
   a.grid = 0;
-  return done(launch_attention(a, (hipStream_t)stream));
+  const hipStream_t s = (hipStream_t)stream;
+  return done(few_rows(a) ? launch_attn_rows(a, s) : launch_attn_tile(a, s));
 }
 
 }  // extern "C"

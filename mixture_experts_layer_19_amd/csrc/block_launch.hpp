@@ -42,13 +42,18 @@ struct AttnArgs {
   const void *q;               // [rows][heads][head_dim], strides in elements
   long long q_row, q_head;
   int heads, group;            // group = heads / kv_heads
-  float scale;                 // times log2(e): the softmax runs on powers of two
+  float scale;                 // > 0, times log2(e): the softmax runs on powers of two
+  uint32_t q_sign;             // xor of every 32-bit word of q: the sign of a negative scale
   int window, sinks;           // window 0: none
   void *out;                   // [rows][heads][head_dim]
   float *part;                 // workspace: partial results of split units
   int grid;                    // workgroups of the launch
 };
-size_t attn_ws_bytes(const KvArgs &c, int heads, int window, int sinks);
-hipError_t launch_attention(const AttnArgs &a, hipStream_t stream);
+// Few query rows a sequence (attn_rows.hip), and many (attn_tile.hip).
+// Workspace bytes first.
+size_t attn_rows_ws_bytes(const AttnArgs &a);
+hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream);
+size_t attn_tile_ws_bytes(const AttnArgs &a);
+hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t stream);
 
 }  // namespace moe
