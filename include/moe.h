@@ -334,8 +334,8 @@ MOE_API moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *res
  * [num_pages][kv_heads][page_size][head_dim] of keys and values.
  * dtype MOE_BF16 or MOE_F32: elements; MOE_MXFP8: E4M3 codes, with E8M0
  * scale bytes [num_pages][kv_heads][page_size][head_dim/32].  page_size: a
- * power of two up to 65536; head_dim 64, 128 or 256.  Activations are bf16
- * (fp32 for a MOE_F32 cache). */
+ * power of two up to 65536; head_dim 64, 128 or 256; num_pages * kv_heads *
+ * page_size below 2^32 - 1.  Activations are bf16 (fp32 for a MOE_F32 cache). */
 typedef struct moe_kv_cache {
   void *k, *v;
   uint8_t *k_scale, *v_scale;    /* MOE_MXFP8 only */
@@ -348,10 +348,11 @@ typedef struct moe_kv_cache {
  * position kv_len[s] - row_offsets[s+1] + r, and position p lies in slot
  * p % page_size of page page_table[s][p / page_size].  Entries that are not a
  * page (negative, or num_pages and above) hold no token.  max_rows: at least
- * the largest number of new tokens of one sequence.  The arrays are read when
+ * the largest number of new tokens of one sequence (the rows of a sequence past
+ * max_rows are not computed).  The arrays are read when
  * the calls run, so a captured graph follows lengths that change; whatever
  * they hold, no access leaves the pools and the activations.
- * max_pages * page_size + rows stays below 2^31. */
+ * max_pages * page_size + rows is at most 2^31 - 4097. */
 typedef struct moe_kv_batch {
   const int32_t *page_table;     /* [seqs][max_pages] */
   const int32_t *row_offsets;    /* [seqs + 1], ascending */

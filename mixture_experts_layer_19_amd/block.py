@@ -22,7 +22,6 @@ refuses raises :class:`.binding.MoeError`.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -35,9 +34,11 @@ _CACHE = {"bf16": (B.MOE_BF16, torch.bfloat16, torch.bfloat16),
           # OCP MX-fp8: E4M3 codes and one E8M0 scale byte per 32 elements of head_dim
           "mxfp8": (B.MOE_MXFP8, torch.uint8, torch.bfloat16)}
 _QUANT = {"none": B.MOE_NO_QUANT, "mxfp8": B.MOE_MXFP8, "fp8": B.MOE_FP8}
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda d: torch.cuda.current_stream(d).cuda_stream)
-_NO_GUARD = contextlib.nullcontext()
+# Small calls are bound by the host, so the checks build no message unless they
+# fail, and the stream and device are asked for without torch's wrappers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _require(ok, what):
@@ -45,11 +46,12 @@ def _require(ok, what):
         raise ValueError(what)
 
 
-def _on(device, stream):
-    """The context in which a call's outputs are allocated and its kernels run."""
+def _elsewhere(index, stream):
+    """A context in which the current device and stream are the call's, or None
+    if they are already."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return None if _current_device() == index else torch.cuda.device(index)
 
 
 def _device(t: torch.Tensor) -> torch.device:
@@ -83,34 +85,38 @@ class RMSNorm:
         self.weight, self.eps, self.quant, self.fp8_scale = weight, float(eps), quant, float(fp8_scale)
         self.hidden = weight.numel()
         self.device = _device(weight)
-        self._q = _QUANT[quant]
+        self._q, self._dtype, self._w = _QUANT[quant], _ACT[weight.dtype], weight.data_ptr()
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, want_y: bool = True,
                  stream=None) -> NormResult:
         """x, residual: [rows, hidden], rows contiguous inside.  want_y False
         leaves y out where there is an 8-bit output."""
         w, hidden = self.weight, self.hidden
+        shape = x.shape
         for t in (x,) if residual is None else (x, residual):
-            _require(t.dim() == 2 and t.shape[1] == hidden and t.dtype == w.dtype and t.device == self.device,
-                     "expected [rows, %d] of %s on %s, got %s of %s on %s"
-                     % (hidden, w.dtype, self.device, list(t.shape), t.dtype, t.device))
-            _require(t.stride(1) == 1 or hidden == 1, "rows must be contiguous")
-        rows = x.shape[0]
-        _require(residual is None or residual.shape[0] == rows, "x and residual differ in rows")
+            if t.dim() != 2 or t.shape != shape or shape[1] != hidden or t.dtype != w.dtype or t.device != self.device:
+                raise ValueError("expected [rows, %d] of %s on %s, got %s of %s on %s"
+                                 % (hidden, w.dtype, self.device, list(t.shape), t.dtype, t.device))
+            if t.stride(1) != 1 and hidden != 1:
+                raise ValueError("rows must be contiguous")
         _require(want_y or self._q != B.MOE_NO_QUANT, "without y there is no output")
-        with _on(self.device, stream):
-            shape = (rows, hidden)
-            new = torch.empty
-            r = None if residual is None else new(shape, dtype=w.dtype, device=self.device)
-            y = new(shape, dtype=w.dtype, device=self.device) if want_y else None
-            q = scale = None
-            if self._q != B.MOE_NO_QUANT:
-                q = new(shape, dtype=torch.uint8, device=self.device)
-                if self._q == B.MOE_MXFP8:
-                    scale = new((rows, hidden // 32), dtype=torch.uint8, device=self.device)
-            B.moe_rms_norm(x, x.stride(0), residual, 0 if residual is None else residual.stride(0), w,
-                           _ACT[w.dtype], rows, hidden, self.eps, r, y, self._q, self.fp8_scale, q, scale,
-                           _raw_stream(self.device.index))
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self(x, residual, want_y=want_y)
+        # empty_like of rows that are contiguous inside is contiguous as a whole
+        r = None if residual is None else torch.empty_like(residual)
+        y = torch.empty_like(x) if want_y else None
+        q = scale = None
+        if self._q != B.MOE_NO_QUANT:
+            q = torch.empty(shape, dtype=torch.uint8, device=self.device)
+            if self._q == B.MOE_MXFP8:
+                scale = torch.empty((shape[0], hidden // 32), dtype=torch.uint8, device=self.device)
+        B.moe_rms_norm(x.data_ptr(), x.stride(0), None if r is None else residual.data_ptr(),
+                       0 if r is None else residual.stride(0), self._w, self._dtype, shape[0], hidden, self.eps,
+                       None if r is None else r.data_ptr(), None if y is None else y.data_ptr(), self._q,
+                       self.fp8_scale, None if q is None else q.data_ptr(),
+                       None if scale is None else scale.data_ptr(), _raw_stream(self.device.index))
         return NormResult(r, y, q, scale)
 
 
@@ -181,31 +187,37 @@ class PagedKVCache:
                               vs.data_ptr() if mx else None, num_pages, page_size, kv_heads, head_dim, code)
 
     def _check(self, batch, t, heads, what):
-        _require(t.shape == (batch.rows, heads, self.head_dim) and t.dtype == self.act_dtype
-                 and t.device == self.device,
-                 "%s must be [%d, %d, %d] of %s on %s, got %s of %s on %s"
-                 % (what, batch.rows, heads, self.head_dim, self.act_dtype, self.device, list(t.shape), t.dtype,
-                    t.device))
-        _require(t.stride(2) == 1, "%s must be contiguous along head_dim" % what)
+        if t.shape != (batch.rows, heads, self.head_dim) or t.dtype != self.act_dtype or t.device != self.device:
+            raise ValueError("%s must be [%d, %d, %d] of %s on %s, got %s of %s on %s"
+                             % (what, batch.rows, heads, self.head_dim, self.act_dtype, self.device, list(t.shape),
+                                t.dtype, t.device))
+        if t.stride(2) != 1:
+            raise ValueError("%s must be contiguous along head_dim" % what)
+        if batch.device != self.device:
+            raise ValueError("the batch is on %s, the cache on %s" % (batch.device, self.device))
 
     def write(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, *, stream=None) -> None:
         """Put the new tokens' k and v [rows, kv_heads, head_dim] (row and head
         strides in whole 16-byte pieces) into their pages."""
         self._check(batch, k, self.kv_heads, "k")
         self._check(batch, v, self.kv_heads, "v")
-        _require(batch.device == self.device, "the batch is on %s, the cache on %s" % (batch.device, self.device))
-        with _on(self.device, stream):
-            B.moe_kv_write(self.c, batch.c, k, k.stride(0), k.stride(1), v, v.stride(0), v.stride(1),
-                           _raw_stream(self.device.index))
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self.write(batch, k, v)
+        B.moe_kv_write(self.c, batch.c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                       v.stride(1), _raw_stream(self.device.index))
 
     def read(self, batch: KVBatch, *, stream=None):
         """The batch's tokens' (k, v) [rows, kv_heads, head_dim], dequantised."""
-        _require(batch.device == self.device, "the batch is on %s, the cache on %s" % (batch.device, self.device))
-        with _on(self.device, stream):
-            shape = (batch.rows, self.kv_heads, self.head_dim)
-            k = torch.empty(shape, dtype=self.act_dtype, device=self.device)
-            v = torch.empty(shape, dtype=self.act_dtype, device=self.device)
-            B.moe_kv_read(self.c, batch.c, k, v, _raw_stream(self.device.index))
+        _require(batch.device == self.device, "the batch and the cache are on different devices")
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self.read(batch)
+        k = torch.empty((batch.rows, self.kv_heads, self.head_dim), dtype=self.act_dtype, device=self.device)
+        v = torch.empty_like(k)
+        B.moe_kv_read(self.c, batch.c, k.data_ptr(), v.data_ptr(), _raw_stream(self.device.index))
         return k, v
 
     def attention(self, batch: KVBatch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
@@ -217,21 +229,23 @@ class PagedKVCache:
         _require(q.dim() == 3, "q must be [rows, heads, head_dim]")
         heads = q.shape[1]
         self._check(batch, q, heads, "q")
-        _require(heads > 0 and heads % self.kv_heads == 0,
-                 "%d heads do not share %d KV heads" % (heads, self.kv_heads))
+        if heads == 0 or heads % self.kv_heads:
+            raise ValueError("%d heads do not share %d KV heads" % (heads, self.kv_heads))
         _require(window >= 0 and sinks >= 0, "window and sinks must not be negative")
-        _require(batch.device == self.device, "the batch is on %s, the cache on %s" % (batch.device, self.device))
+        if out is not None:
+            self._check(batch, out, heads, "out")
+            _require(out.is_contiguous(), "out must be contiguous")
         # the library counts positions in 32 bits: a larger window hides nothing either
         window, sinks = min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF)
-        with _on(self.device, stream):
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-            else:
-                self._check(batch, out, heads, "out")
-                _require(out.is_contiguous(), "out must be contiguous")
-            n = B.moe_attention_workspace_bytes(self.c, batch.c, heads, window, sinks)
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-            B.moe_attention(self.c, batch.c, q, q.stride(0), q.stride(1), heads,
-                            self.head_dim ** -0.5 if scale is None else scale, window, sinks, out, ws, n,
-                            _raw_stream(self.device.index))
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self.attention(batch, q, scale, window, sinks, out=out)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        n = B.moe_attention_workspace_bytes(self.c, batch.c, heads, window, sinks)
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        B.moe_attention(self.c, batch.c, q.data_ptr(), q.stride(0), q.stride(1), heads,
+                        self.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+                        None if ws is None else ws.data_ptr(), n, _raw_stream(self.device.index))
         return out

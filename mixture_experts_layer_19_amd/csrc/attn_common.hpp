@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t word_finite(uint32_t w) {
 }
 // What is not finite of elements [d, d + 4) of pool row r, zero elsewhere.
 template <int F, int HD>
-__device__ __forceinline__ f32x4 not_finite4(const KvArgs &c, long long r, int d) {
-  const long long at = r * HD + d;
+__device__ __forceinline__ f32x4 not_finite4(const KvArgs &c, uint32_t r, int d) {
+  const long long at = (long long)r * HD + d;
   f32x4 v;
   if constexpr (F == FMT_F32) {
     v = *(const f32x4 *)(c.v + 4 * at);

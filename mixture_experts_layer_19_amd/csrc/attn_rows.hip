@@ -44,6 +44,9 @@ struct RowsCfg {
   static constexpr int o_pitch = HD * 4 + 16, o_bytes = rows * o_pitch;
   static constexpr int wave_bytes = v_bytes > o_bytes ? v_bytes : o_bytes;
   static constexpr int lds = 4 * wave_bytes + 4 * rows * 8;
+  // two workgroups a CU where the registers suffice: the one's loads run under
+  // the other's products
+  static constexpr int occupancy = RT == 1 && HD <= 128 ? 2 : 1;
 };
 
 // The even cut of the tiles of all units.  Unit order: sequence, row tile,
@@ -51,7 +54,8 @@ struct RowsCfg {
 template <int BK, int ROWS>
 struct Cut {
   const AttnArgs &a;
-  __device__ __forceinline__ Cut(const AttnArgs &args) : a(args) {}
+  int sums0;                   // scan(0)
+  __device__ __forceinline__ Cut(const AttnArgs &args) : a(args), sums0(sums(0)) {}
   __device__ __forceinline__ static int row_tiles(const AttnArgs &a, const SeqGeo &g) {
     return (int)(((long long)g.n * a.group + ROWS - 1) / ROWS);
   }
@@ -65,7 +69,7 @@ struct Cut {
     return g.n ? row_tiles(a, g) * tiles(a, g) : 0;
   }
   // inclusive sums of 64 sequences' weights from s0 on, one a lane
-  __device__ __forceinline__ int scan(int s0) const {
+  __device__ __forceinline__ int sums(int s0) const {
     const int lane = threadIdx.x & 63;
     int v = weight(s0 + lane);
 #pragma unroll
@@ -75,30 +79,30 @@ struct Cut {
     }
     return v;
   }
-  __device__ __forceinline__ long long total() const {
-    long long t = 0;
+  __device__ __forceinline__ int scan(int s0) const { return s0 ? sums(s0) : sums0; }
+  __device__ __forceinline__ int total() const {
+    int t = 0;
     for (int s0 = 0; s0 < a.c.seqs; s0 += 64) t += __shfl(scan(s0), 63, 64);
     return t * a.c.kv_heads;
   }
   // sequence that holds position x, and the position of its first tile
-  __device__ __forceinline__ int find(long long x, long long &start) const {
-    long long t = 0;
+  __device__ __forceinline__ int find(int x, int &start) const {
+    int t = 0;
     for (int s0 = 0; s0 < a.c.seqs; s0 += 64) {
       const int v = scan(s0);
-      const int sum = __shfl(v, 63, 64);
-      if ((t + sum) * a.c.kv_heads > x) {
-        const unsigned long long past = __ballot((t + v) * a.c.kv_heads > x);
+      const unsigned long long past = __ballot((t + v) * a.c.kv_heads > x);
+      if (past) {
         const int l = __ffsll((long long)past) - 1;
         start = (t + (l ? __shfl(v, l - 1, 64) : 0)) * a.c.kv_heads;
         return s0 + l;
       }
-      t += sum;
+      t += __shfl(v, 63, 64);
     }
     return -1;
   }
   // first position of sequence s
-  __device__ __forceinline__ long long first(int s) const {
-    long long t = 0;
+  __device__ __forceinline__ int first(int s) const {
+    int t = 0;
     for (int s0 = 0; s0 < a.c.seqs; s0 += 64) {
       const int v = scan(s0);
       if (s < s0 + 64) return (t + (s > s0 ? __shfl(v, s - s0 - 1, 64) : 0)) * a.c.kv_heads;
@@ -107,17 +111,20 @@ struct Cut {
     return t * a.c.kv_heads;
   }
 };
-// first position of workgroup w's run; the workgroup that holds position x
-__device__ __forceinline__ long long run_start(long long total, int w, int runs) { return total * w / runs; }
-__device__ __forceinline__ int run_of(long long total, long long x, int runs) {
-  int w = (int)(x * runs / total);
-  while (w + 1 < runs && run_start(total, w + 1, runs) <= x) ++w;
-  while (w > 0 && run_start(total, w, runs) > x) --w;
-  return w;
-}
+// The runs: the first `more` of them hold one tile more than the others.
+struct Runs {
+  int n, len, more;
+  __device__ __forceinline__ Runs(int total, int grid)
+      : n(min(grid, total)), len(n ? total / n : 0), more(n ? total % n : 0) {}
+  __device__ __forceinline__ int start(int w) const { return w * len + min(w, more); }
+  __device__ __forceinline__ int of(int x) const {
+    const int cut = more * (len + 1);
+    return x < cut ? x / (len + 1) : more + (x - cut) / len;
+  }
+};
 
 template <int F, int HD, int RT, int NKH>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void attn_rows_kernel(AttnArgs a) {
   using C = RowsCfg<F, HD, RT, NKH>;
   using R = typename C::R;
   constexpr int BK = C::BK, ROWS = C::rows, DT = HD / 16;
@@ -129,20 +136,19 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
   const KvArgs &c = a.c;
 
   const Cut<BK, ROWS> cut(a);
-  const long long total = cut.total();
-  const int runs = (int)min((long long)a.grid, total);     // no run is empty
-  if ((int)blockIdx.x >= runs) return;
-  long long x = run_start(total, blockIdx.x, runs);
-  const long long x_begin = x, x_end = run_start(total, blockIdx.x + 1, runs);
+  const Runs runs(__builtin_amdgcn_readfirstlane(cut.total()), a.grid);
+  const bool idle = (int)blockIdx.x >= runs.n;
+  const int x_begin = idle ? 0 : runs.start(blockIdx.x), x_end = idle ? 0 : runs.start(blockIdx.x + 1);
 
-  while (x < x_end) {
-    long long seq_x;
+  for (int x = x_begin; x < x_end;) {
+    int seq_x;
     const int s = __builtin_amdgcn_readfirstlane(cut.find(x, seq_x));
-    const SeqGeo g = seq_geo(c, s);
+    const SeqGeo g = uniform(seq_geo(c, s));
     const KeyRange<BK> range(g, 0, g.n - 1, a.window, a.sinks);
     const int T = max(range.tiles, 1);
-    const int unit = (int)((x - seq_x) / T), t0 = (int)((x - seq_x) % T);
-    const int t1 = (int)min((long long)T, t0 + (x_end - x));
+    const int in_seq = x - __builtin_amdgcn_readfirstlane(seq_x);
+    const int unit = in_seq / T, t0 = in_seq % T;
+    const int t1 = min(T, t0 + (x_end - x));
     const int h = unit % c.kv_heads, rt0 = unit / c.kv_heads * ROWS;   // first row of the tile
     const int nrows = g.n * a.group;
 
@@ -175,22 +181,26 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
       for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0, 0, 0, 0};
     }
 
-    // the wave's tile t: its keys, their pages, their rows in the pool
+    // The wave's tile t: its keys' entries of the table, their rows in the pool.
+    // No load of the loop stands under a condition (past the last tile row 0 of
+    // the pool is read again): with a load that may or may not have been issued,
+    // waiting for an older one would be waiting for all.
     const int32_t *pages = c.table + (long long)s * c.max_pages;
     int page[NKH];
     auto load_pages = [&](int t) MOE_INLINE {
+      const int k0 = range.key(min(t, t1 - 1)) + wave * C::keys;
+#pragma unroll
+      for (int kh = 0; kh < NKH; ++kh)
+        page[kh] = pages[min((k0 + 16 * kh + l16) >> c.page_shift, c.max_pages - 1)];
+    };
+    uint32_t row[NKH];
+    auto rows_of = [&](int t) MOE_INLINE {
       const int k0 = range.key(t) + wave * C::keys;
 #pragma unroll
       for (int kh = 0; kh < NKH; ++kh) {
         const int key = k0 + 16 * kh + l16;
-        page[kh] = key < g.len ? pages[key >> c.page_shift] : -1;
+        row[kh] = t < t1 && key < g.len ? pool_row(c, page[kh], h, key) : kNoRow;
       }
-    };
-    long long row[NKH];
-    auto rows_of = [&](int t) MOE_INLINE {
-      const int k0 = range.key(t) + wave * C::keys;
-#pragma unroll
-      for (int kh = 0; kh < NKH; ++kh) row[kh] = pool_row(c, page[kh], h, k0 + 16 * kh + l16);
     };
     i32x4 kr[NKH][R::pieces], vr[NKH][R::pieces];
     uint32_t ks[NKH][R::scales], vs[NKH][R::scales];
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
                          uint32_t (&sc)[NKH][R::scales]) MOE_INLINE {
 #pragma unroll
       for (int kh = 0; kh < NKH; ++kh) {
-        const long long r = row[kh] < 0 ? 0 : row[kh];
+        const long long r = row[kh] == kNoRow ? 0 : row[kh];
         const uint8_t *p = pool + r * R::bytes + (F == FMT_MX8 ? HD / 4 * g4 : 16 * g4);
 #pragma unroll
         for (int i = 0; i < R::pieces; ++i)
@@ -235,6 +245,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
             put(dst + 64 * p + 16 * g4, __builtin_bit_cast(uint4, vr[kh][p]));
           }
         });
+        if constexpr (F == FMT_MX8 && kh % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       });
     };
     // The wave's LDS accesses before this point come before those after it.
@@ -287,8 +298,8 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     };
     auto add_not_finite = [&](int k0) MOE_INLINE {
       for (int key = k0; key < k0 + C::keys && key < g.len; ++key) {
-        const long long r = pool_row(c, pages[key >> c.page_shift], h, key);
-        if (r < 0) continue;
+        const uint32_t r = pool_row(c, pages[key >> c.page_shift], h, key);
+        if (r == kNoRow) continue;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const f32x4 v = not_finite4<F, HD>(c, r, 16 * d + 4 * g4);
@@ -318,24 +329,28 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
         for (int i = 0; i < R::scales; ++i) bad = bad || sb[i] >= kScaleOverflow;
       return bad;
     };
-    // tokens of the row tile
+    // tokens of the row tile, and the keys that all of them see
     const int tok_a = rt0 / a.group, tok_b = (min(rt0 + ROWS, nrows) - 1) / a.group;
+    const int all_hi = min(g.pos0 + tok_a + 1, g.len), all_lo = a.window ? g.pos0 + tok_b - a.window + 1 : 0;
 
+    // in the loop's order: its waits count the loads issued since
     load_pages(t0);
     rows_of(t0);
     load_rows(c.k, c.k_scale, kr, ks);
+    __builtin_amdgcn_sched_barrier(0);
+    load_pages(t0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
     load_rows(c.v, c.v_scale, vr, vs);
-    if (t0 + 1 < t1) load_pages(t0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
 
     for (int t = t0; t < t1; ++t) {
       const int k0 = range.key(t) + wave * C::keys;
-      const bool more = t + 1 < t1;
       // keys that exist: bit l of half kh is key k0 + 16 kh + l
       uint32_t there[NKH];
       bool all = true;
 #pragma unroll
       for (int kh = 0; kh < NKH; ++kh) {
-        const unsigned long long m = __ballot(row[kh] >= 0);
+        const unsigned long long m = __ballot(row[kh] != kNoRow);
         there[kh] = (uint32_t)m & 0xFFFFu;
         all = all && there[kh] == 0xFFFFu;
       }
@@ -372,50 +387,66 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
                     __int_as_float(kr[kh][p][e]), __int_as_float(q[rt][p][e]), sc[rt][kh], 0, 0, 0);
           }
         });
+        // codes of two halves at a time become bf16: more would not fit the registers
+        if constexpr (F == FMT_MX8 && kh % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       });
       __builtin_amdgcn_sched_barrier(0);
-      if (more) {
-        rows_of(t + 1);
-        load_rows(c.k, c.k_scale, kr, ks);
-      }
+      rows_of(t + 1);
+      load_rows(c.k, c.k_scale, kr, ks);
+      __builtin_amdgcn_sched_barrier(0);
+      // before V's loads: waiting for the pages, which the next K needs, is then
+      // not waiting for V
+      load_pages(t + 2);
       __builtin_amdgcn_sched_barrier(0);
 
       // softmax over the tile; sc becomes the weights
+      const bool inner = all && k0 + C::keys <= all_hi && (k0 >= all_lo || k0 + C::keys <= a.sinks);
+      if (!inner) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int kh = 0; kh < NKH; ++kh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = 4 * g4 + i, key = k0 + 16 * kh + j;
+              const bool see = ((there[kh] >> j) & 1) && key < hi[rt] && (key >= lo[rt] || key < a.sinks);
+              sc[rt][kh][i] = see ? sc[rt][kh][i] : -INFINITY;
+            }
+      }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float top = mx[rt];
+        float top = -INFINITY;
 #pragma unroll
         for (int kh = 0; kh < NKH; ++kh)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 4 * g4 + i, key = k0 + 16 * kh + j;
-            const bool see = ((there[kh] >> j) & 1) && key < hi[rt] && (key >= lo[rt] || key < a.sinks);
-            const float v = see ? sc[rt][kh][i] * a.scale : -INFINITY;
-            sc[rt][kh][i] = v;
-            top = fmaxf(top, v);
-          }
-        top = max_rows16(top);
-        const float alpha = __builtin_amdgcn_exp2f(mx[rt] - top);
-        mx[rt] = top;
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[rt][kh][i]);
+        top = max_rows16(top) * a.scale;           // the scale is positive
+        // the reference moves only when a score passes it by 2^8
+        if (__ballot(top > mx[rt] + 8.0f)) {
+          const float now = top > mx[rt] + 8.0f ? top : mx[rt];
+          const float alpha = __builtin_amdgcn_exp2f(mx[rt] - now);
+          mx[rt] = now;
+          sum[rt] *= alpha;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[rt][d] *= alpha;
+        }
         float part = 0.0f;
 #pragma unroll
         for (int kh = 0; kh < NKH; ++kh)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = __builtin_amdgcn_exp2f(sc[rt][kh][i] - top);
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[rt][kh][i], a.scale, -mx[rt]));
             sc[rt][kh][i] = p;
             part += p;
           }
-        sum[rt] = sum[rt] * alpha + part;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[rt][d] *= alpha;
+        sum[rt] += part;
       }
 
       // V of keys that do not exist: zeros (their weight is zero, but zero times
       // what a free page holds need not be)
       if (!all)
         static_for<NKH>([&](auto kh) MOE_INLINE {
-          if (row[kh] < 0) clear_v(vr[kh], vs[kh]);
+          if (!((there[kh] >> l16) & 1)) clear_v(vr[kh], vs[kh]);
         });
       // keys that some rows of the tile see and others do not
       bool unsafe = false;
@@ -425,10 +456,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
       if (fix) store_v(std::true_type{});
       else store_v(std::false_type{});
       __builtin_amdgcn_sched_barrier(0);
-      if (more) {
-        load_rows(c.v, c.v_scale, vr, vs);
-        if (t + 2 < t1) load_pages(t + 2);
-      }
+      load_rows(c.v, c.v_scale, vr, vs);
       wave_sync();
       add_pv();
       if (fix) add_not_finite(k0);
@@ -487,73 +515,93 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     __syncthreads();
     x += t1 - t0;
   }
+  clear_free_rows<F, HD>(a);
 }
 
-// Join the pieces of cut units: a workgroup takes kJoinRows rows of a unit,
-// 256 / (HD / 4) threads wide along the pieces.  It also clears the rows of
-// no sequence.
-constexpr int kJoinRows = 4;
-
+// Join the pieces of cut units, 4 columns a thread.  With few units a
+// workgroup takes one row (`per` = 1), its 256 / COLS groups of threads every
+// SL-th piece each; with many it takes SL rows (`per` = SL), one a group, since
+// a unit then has few pieces.
 template <int F, int HD, int RT, int NKH>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int units) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit_rows, int units, int per) {
   using C = RowsCfg<F, HD, RT, NKH>;
-  constexpr int BK = C::BK, ROWS = C::rows, QUADS = ROWS / kJoinRows;
-  constexpr int COLS = HD / 4, SL = 256 / COLS;    // columns of 4, slices of the pieces
+  constexpr int BK = C::BK, ROWS = C::rows;
+  constexpr int COLS = HD / 4, SL = 256 / COLS;
   __shared__ f32x4 red[256];
   __shared__ float redm[SL][2];
   const KvArgs &c = a.c;
   const int tid = threadIdx.x, col = tid % COLS, sl = tid / COLS;
-  clear_free_rows<F, HD>(a);
-  const int quad = blockIdx.x % QUADS, h = blockIdx.x / QUADS % c.kv_heads;
-  const int s = blockIdx.x / QUADS / c.kv_heads / units, rt = blockIdx.x / QUADS / c.kv_heads % units;
-  const SeqGeo g = seq_geo(c, s);
-  const int nrows = g.n * a.group, m0 = rt * ROWS + quad * kJoinRows;
-  if (m0 >= nrows) return;
+  const int parts = (unit_rows + per - 1) / per;
+  const int unit = blockIdx.x / parts, h = unit % c.kv_heads;
+  const int s = unit / c.kv_heads / units, rt = unit / c.kv_heads % units;
+  const int m = blockIdx.x % parts * per + (per == 1 ? 0 : sl);
   const Cut<BK, ROWS> cut(a);
-  const long long total = cut.total();
-  const int runs = (int)min((long long)a.grid, total);
+  const SeqGeo g = uniform(seq_geo(c, s));
+  const int nrows = g.n * a.group - rt * ROWS;      // of this unit
+  if (nrows <= 0) return;
+  const Runs runs(__builtin_amdgcn_readfirstlane(cut.total()), a.grid);
   const int T = Cut<BK, ROWS>::tiles(a, g);
-  const long long x0 = cut.first(s) + (long long)(rt * c.kv_heads + h) * T, x1 = x0 + T;
-  const int w0 = run_of(total, x0, runs), w1 = run_of(total, x1 - 1, runs);
+  const int x0 = __builtin_amdgcn_readfirstlane(cut.first(s)) + (rt * c.kv_heads + h) * T;
+  const int w0 = runs.of(x0), w1 = runs.of(x0 + T - 1);
   if (w0 == w1) return;                            // never cut: its workgroup wrote it
-  const int first_slot = 2 * w0 + (run_start(total, w0, runs) == x0 ? 0 : 1);
-  for (int mi = 0; mi < kJoinRows && m0 + mi < nrows; ++mi) {
-    const int m = quad * kJoinRows + mi;
-    float top = kNegBig, l = 0.0f;
-    f32x4 acc = {0, 0, 0, 0};
-    for (int w = w0 + sl; w <= w1; w += SL) {
-      const float *p = a.part + (long long)(w == w0 ? first_slot : 2 * w) * ROWS * (HD + 2);
-      const float pm = p[ROWS * HD + 2 * m], pl = p[ROWS * HD + 2 * m + 1];
-      const f32x4 po = *(const f32x4 *)(p + m * HD + 4 * col);
-      const float nt = fmaxf(top, pm);
-      const float e0 = __builtin_amdgcn_exp2f(top - nt), e1 = __builtin_amdgcn_exp2f(pm - nt);
-      acc = acc * e0 + po * e1;
-      l = l * e0 + pl * e1;
-      top = nt;
+  const int first_slot = 2 * w0 + (runs.start(w0) == x0 ? 0 : 1);
+  const bool in = m < min(nrows, ROWS) && m < unit_rows;
+  const int mr = in ? m : 0;
+  float top = kNegBig, l = 0.0f;
+  f32x4 acc = {0, 0, 0, 0};
+  constexpr int AHEAD = 4;                         // pieces in flight a thread
+  const int step = per == 1 ? SL : 1;
+  for (int w = w0 + (per == 1 ? sl : 0); w <= w1; w += AHEAD * step) {
+    float pm[AHEAD], pl[AHEAD];
+    f32x4 po[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int wi = min(w + i * step, w1);
+      const float *p = a.part + (long long)(wi == w0 ? first_slot : 2 * wi) * ROWS * (HD + 2);
+      pm[i] = p[ROWS * HD + 2 * mr];
+      pl[i] = p[ROWS * HD + 2 * mr + 1];
+      po[i] = *(const f32x4 *)(p + mr * HD + 4 * col);
     }
-    __syncthreads();
+    float nt = top;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) nt = fmaxf(nt, w + i * step <= w1 ? pm[i] : kNegBig);
+    const float e0 = __builtin_amdgcn_exp2f(top - nt);
+    acc *= e0;
+    l *= e0;
+    top = nt;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (w + i * step <= w1) {
+        const float e = __builtin_amdgcn_exp2f(pm[i] - nt);
+        acc += po[i] * e;
+        l += pl[i] * e;
+      }
+  }
+  if (per == 1) {
     red[tid] = acc;
     if (col == 0) { redm[sl][0] = top; redm[sl][1] = l; }
     __syncthreads();
-    if (sl == 0) {
-      float mt = kNegBig, lt = 0.0f;
-      f32x4 at4 = {0, 0, 0, 0};
-      for (int i = 0; i < SL; ++i) mt = fmaxf(mt, redm[i][0]);
-      for (int i = 0; i < SL; ++i) {
-        const float e = __builtin_amdgcn_exp2f(redm[i][0] - mt);
-        lt += e * redm[i][1];
-        at4 += e * red[i * COLS + col];
-      }
-      const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-      at4 *= inv;
-      const int tok = (rt * ROWS + m) / a.group, hq = h * a.group + (rt * ROWS + m) % a.group;
-      const long long at = ((long long)(g.r0 + tok) * a.heads + hq) * HD + 4 * col;
-      if constexpr (F == FMT_F32)
-        *(f32x4 *)((float *)a.out + at) = at4;
-      else
-        *(uint2 *)((uint16_t *)a.out + at) = make_uint2(bf16_pack2(at4[0], at4[1]), bf16_pack2(at4[2], at4[3]));
+    if (sl) return;
+    top = kNegBig;
+    l = 0.0f;
+    acc = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < SL; ++i) top = fmaxf(top, redm[i][0]);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const float e = __builtin_amdgcn_exp2f(redm[i][0] - top);
+      l += e * redm[i][1];
+      acc += e * red[i * COLS + col];
     }
   }
+  if (!in) return;
+  acc *= l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = (rt * ROWS + m) / a.group, hq = h * a.group + (rt * ROWS + m) % a.group;
+  const long long at = ((long long)(g.r0 + tok) * a.heads + hq) * HD + 4 * col;
+  if constexpr (F == FMT_F32)
+    *(f32x4 *)((float *)a.out + at) = acc;
+  else
+    *(uint2 *)((uint16_t *)a.out + at) = make_uint2(bf16_pack2(acc[0], acc[1]), bf16_pack2(acc[2], acc[3]));
 }
 
 namespace {
@@ -565,10 +613,17 @@ struct Launch {
   static int units(const KvArgs &c, int group) {   // row tiles of the longest sequence
     return (int)(((long long)c.max_rows * group + C::rows - 1) / C::rows);
   }
-  static int grid(const KvArgs &c, int group) {
+  // tiles of all units, at most; -1 past 32 bits, which the kernels count in
+  static long long most(const KvArgs &c, int group) {
     const long long tiles = (((long long)c.max_pages << c.page_shift) + C::BK - 1) / C::BK + 1;
-    const long long all = (long long)c.seqs * c.kv_heads * units(c, group) * tiles;
-    return (int)(all < kRowsGrid ? all : kRowsGrid);
+    const long long sums = tiles * units(c, group);
+    if (sums > INT32_MAX) return -1;
+    const long long seq = sums * c.kv_heads;
+    return seq > INT32_MAX || seq * c.seqs > INT32_MAX ? -1 : seq * c.seqs;
+  }
+  static int grid(const KvArgs &c, int group) {
+    const long long all = most(c, group);
+    return (int)(all >= 0 && all < kRowsGrid ? all : kRowsGrid);
   }
   static size_t ws(const KvArgs &c, int group) {
     return (size_t)grid(c, group) * 2 * C::rows * (HD + 2) * sizeof(float);
@@ -581,9 +636,12 @@ struct Launch {
     if (once != hipSuccess) return once;
     attn_rows_kernel<F, HD, RT, NKH><<<a.grid, 256, C::lds, s>>>(a);
     const int u = units(a.c, a.group);
-    const long long joins = (long long)a.c.seqs * a.c.kv_heads * u * (C::rows / kJoinRows);
-    if (joins > INT32_MAX) return hipErrorInvalidValue;
-    attn_join_kernel<F, HD, RT, NKH><<<(unsigned)joins, 256, 0, s>>>(a, u);
+    // rows of a unit, at most
+    const long long rows = (long long)a.c.max_rows * a.group;
+    const int unit_rows = (int)(rows < C::rows ? rows : C::rows);
+    const long long all = (long long)a.c.seqs * a.c.kv_heads * u;
+    const int per = all < 256 ? 1 : 1024 / HD;
+    attn_join_kernel<F, HD, RT, NKH><<<(unsigned)(all * ((unit_rows + per - 1) / per)), 256, 0, s>>>(a, unit_rows, u, per);
     return hipGetLastError();
   }
 };
@@ -611,7 +669,7 @@ auto pick(const KvArgs &c, int group, Fn &&f) {
 }  // namespace
 
 size_t attn_rows_ws_bytes(const AttnArgs &a) {
-  return pick(a.c, a.group, [&](auto l) { return l.ws(a.c, a.group); });
+  return pick(a.c, a.group, [&](auto l) -> size_t { return l.most(a.c, a.group) < 0 ? 0 : l.ws(a.c, a.group); });
 }
 hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t s) {
   return pick(a.c, a.group, [&](auto l) { return l.run(a, s); });

@@ -84,15 +84,14 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
   const int tid = threadIdx.x, lane = tid & 63, q32 = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const KvArgs &c = a.c;
-  clear_free_rows<F, HD>(a);
 
   const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % splits;
   const int u = blockIdx.x / c.kv_heads / splits;
   int s, rt;
   find_unit<ROWS>(a, u, s, rt);
   s = __builtin_amdgcn_readfirstlane(s);
-  if (s < 0) return;
-  const SeqGeo g = seq_geo(c, s);
+  if (s < 0) return clear_free_rows<F, HD>(a);
+  const SeqGeo g = uniform(seq_geo(c, s));
   const int nrows = g.n * a.group, rt0 = __builtin_amdgcn_readfirstlane(rt) * ROWS;
   const int tok_a = rt0 / a.group, tok_b = (min(rt0 + ROWS, nrows) - 1) / a.group;
   const KeyRange<BK> range(g, tok_a, tok_b, a.window, a.sinks);
@@ -149,8 +148,8 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
     const int k0 = range.key(t);
     if constexpr (F == FMT_MX8) {
       const int key = mx_key(), part = tid % (256 / BK);
-      const long long r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
-      const long long at = (r < 0 ? 0 : r) * HD + part * C::codes;
+      const uint32_t r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
+      const long long at = (long long)(r == kNoRow ? 0 : r) * HD + part * C::codes;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         kst[p] = *(const i32x4 *)(c.k + at + 16 * p);
@@ -158,7 +157,7 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
       }
       kss = c.k_scale[at >> 5];
       vss = c.v_scale[at >> 5];
-      if (r < 0) {
+      if (r == kNoRow) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) kst[p] = vst[p] = i32x4{0, 0, 0, 0};
         kss = vss = 0;
@@ -167,10 +166,10 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int id = p * 256 + tid, key = id / C::chunks, ch = id % C::chunks;
-        const long long r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
+        const uint32_t r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
         const uint8_t *zero = (const uint8_t *)zero_row;
-        const uint8_t *kp = r < 0 ? zero : c.k + r * C::row_bytes + 16 * ch;
-        const uint8_t *vp = r < 0 ? zero : c.v + r * C::row_bytes + 16 * ch;
+        const uint8_t *kp = r == kNoRow ? zero : c.k + (long long)r * C::row_bytes + 16 * ch;
+        const uint8_t *vp = r == kNoRow ? zero : c.v + (long long)r * C::row_bytes + 16 * ch;
         kst[p] = *(const i32x4 *)kp;
         vst[p] = *(const i32x4 *)vp;
       }
@@ -285,8 +284,8 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 
   auto add_not_finite = [&](int k0) MOE_INLINE {
     for (int key = k0; key < k0 + BK && key < g.len; ++key) {
-      const long long r = pool_row(c, pages[key >> c.page_shift], h, key);
-      if (r < 0) continue;
+      const uint32_t r = pool_row(c, pages[key >> c.page_shift], h, key);
+      if (r == kNoRow) continue;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -421,10 +420,10 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
       }
     }
   }
+  clear_free_rows<F, HD>(a);
 }
 
-// Join the splits of a unit: a wave a row, 4 columns a lane (and more for
-// head_dim 256).
+// Join the splits of a unit: HD / 4 threads a row, 4 columns each.
 template <int F, int HD, int BK, int QT>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int splits) {
   constexpr int ROWS = TileCfg<F, HD, BK, QT>::rows, COLS = HD / 4, PER = 256 / COLS;
@@ -479,6 +478,10 @@ struct TileLaunch {
     const long long s = want / wgs;
     return (int)(s < 1 ? 1 : s < most ? s : most);
   }
+  static bool fits(const AttnArgs &a) {
+    const long long u = units(a) * a.c.kv_heads;
+    return u * splits(a) <= INT32_MAX && u * (C::rows / (1024 / HD)) <= INT32_MAX;
+  }
   static size_t ws(const AttnArgs &a) {
     const int s = splits(a);
     return s == 1 ? 0 : (size_t)units(a) * a.c.kv_heads * s * C::rows * (HD + 2) * sizeof(float);
@@ -486,7 +489,6 @@ struct TileLaunch {
   static hipError_t run(const AttnArgs &a, hipStream_t st) {
     const int s = splits(a);
     const long long u = units(a) * a.c.kv_heads, grid = u * s;
-    if (grid > INT32_MAX || u * (C::rows / (1024 / HD)) > INT32_MAX) return hipErrorInvalidValue;
     static const hipError_t once = hipFuncSetAttribute((const void *)attn_tile_kernel<F, HD, BK, QT, OCC>,
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
     if (once != hipSuccess) return once;
@@ -517,6 +519,9 @@ auto pick_tile(const KvArgs &c, Fn &&f) {
 
 size_t attn_tile_ws_bytes(const AttnArgs &a) {
   return pick_tile(a.c, [&](auto l) { return l.ws(a); });
+}
+bool attn_tile_fits(const AttnArgs &a) {
+  return pick_tile(a.c, [&](auto l) { return l.fits(a); });
 }
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s) {
   return pick_tile(a.c, [&](auto l) { return l.run(a, s); });

@@ -31,7 +31,10 @@ moe_status kv_args(const moe_kv_cache *c, const moe_kv_batch *b, KvArgs *o) {
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_UNSUPPORTED;
   o->page_shift = shift_of(c->page_size);
   if (o->page_shift < 0) return MOE_ERR_UNSUPPORTED;
-  if (((long long)b->max_pages << o->page_shift) + b->rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // positions, and those of a tile past the last key, are int32
+  if (((long long)b->max_pages << o->page_shift) + b->rows > INT32_MAX - 4096) return MOE_ERR_UNSUPPORTED;
+  if ((unsigned long long)c->num_pages * c->kv_heads * c->page_size >= 0xFFFFFFFFull)
+    return MOE_ERR_UNSUPPORTED;
   o->fmt = c->dtype == MOE_F32 ? FMT_F32 : c->dtype == MOE_BF16 ? FMT_BF16 : FMT_MX8;
   o->k = (uint8_t *)c->k;
   o->v = (uint8_t *)c->v;
@@ -155,6 +158,7 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   if (!q || !out || !al(q, 16) || !al(out, 16) || !al(ws, 16) || !strides_ok(a.c, q_row, q_head))
     return MOE_ERR_INVALID_ARG;
   const size_t need = workspace(a);
+  if (few_rows(a) ? need == 0 : !attn_tile_fits(a)) return MOE_ERR_UNSUPPORTED;
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   a.q = q;
   a.q_row = q_row;

@@ -73,8 +73,18 @@ __device__ __forceinline__ SeqGeo seq_geo(const KvArgs &c, int s) {
   g.r0 = min(max(o0, 0), c.rows);
   g.n = min(max(o1, g.r0), c.rows) - g.r0;
   g.pos0 = kvl - g.n;
+  g.n = min(g.n, c.max_rows);      // the launch holds no more
   const long long cap = (long long)c.max_pages << c.page_shift;
   g.len = (int)min((long long)kvl, cap);
+  return g;
+}
+
+// The same in scalar registers (all lanes hold the same).
+__device__ __forceinline__ SeqGeo uniform(SeqGeo g) {
+  g.r0 = __builtin_amdgcn_readfirstlane(g.r0);
+  g.n = __builtin_amdgcn_readfirstlane(g.n);
+  g.pos0 = __builtin_amdgcn_readfirstlane(g.pos0);
+  g.len = __builtin_amdgcn_readfirstlane(g.len);
   return g;
 }
 
@@ -93,12 +103,14 @@ __device__ __forceinline__ int seq_of_row(const KvArgs &c, int r) {
   return s >= 0 && s < c.seqs ? s : -1;
 }
 
-// Index of a key's row in the pool, ((page * kv_heads + head) * page_size +
-// slot), or -1 where the table holds no page for it.
-__device__ __forceinline__ long long pool_row(const KvArgs &c, int page, int head, int key) {
-  if ((unsigned)page >= (unsigned)c.num_pages) return -1;
-  return ((((long long)page * c.kv_heads + head) << c.page_shift) |
-          (key & ((1 << c.page_shift) - 1)));
+// Index of a key's row in the pool, (page * kv_heads + head) * page_size +
+// slot, or kNoRow where the table holds no page for it.  (A pool has fewer
+// than 2^32 - 1 rows.)
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t pool_row(const KvArgs &c, int page, int head, int key) {
+  if ((unsigned)page >= (unsigned)c.num_pages) return kNoRow;
+  return (((uint32_t)page * (uint32_t)c.kv_heads + (uint32_t)head) << c.page_shift) |
+         ((uint32_t)key & ((1u << c.page_shift) - 1u));
 }
 
 }  // namespace moe

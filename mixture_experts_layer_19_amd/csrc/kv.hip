@@ -21,11 +21,11 @@ struct KvIo {
 
 constexpr int kKvRows = 4;     // rows of a workgroup
 
-// Place of each of the workgroup's rows in the pool, head 0 (-1: none).
-__device__ __forceinline__ void find_rows(const KvArgs &c, int row0, long long *place) {
+// Place of each of the workgroup's rows in the pool, head 0 (kNoRow: none).
+__device__ __forceinline__ void find_rows(const KvArgs &c, int row0, uint32_t *place) {
   const int wave = threadIdx.x >> 6;
   const int r = row0 + wave;
-  long long p = -1;
+  uint32_t p = kNoRow;
   if (r < c.rows) {
     const int s = seq_of_row(c, r);
     if (s >= 0) {
@@ -40,7 +40,7 @@ __device__ __forceinline__ void find_rows(const KvArgs &c, int row0, long long *
 
 template <int F>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
-  __shared__ long long place[kKvRows];
+  __shared__ uint32_t place[kKvRows];
   const int row0 = blockIdx.x * kKvRows;
   find_rows(c, row0, place);
   __syncthreads();
@@ -50,10 +50,10 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
     const int rr = i / (2 * per_side), in = i % (2 * per_side), side = in / per_side;
     const int h = in % per_side / per_head, d = in % per_head * E, r = row0 + rr;
     if (r >= c.rows) break;
-    const long long at = place[rr];
-    if (at < 0) continue;
+    const uint32_t at = place[rr];
+    if (at == kNoRow) continue;
     const long long src = side ? r * io.v_row + h * io.v_head + d : r * io.k_row + h * io.k_head + d;
-    const long long dst = (at + ((long long)h << c.page_shift)) * c.head_dim + d;
+    const long long dst = (long long)(at + ((uint32_t)h << c.page_shift)) * c.head_dim + d;
     uint8_t *pool = side ? c.v : c.k;
     const void *from = side ? io.v : io.k;
     if constexpr (F == FMT_F32) {
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
 
 template <int F>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, KvIo io) {
-  __shared__ long long place[kKvRows];
+  __shared__ uint32_t place[kKvRows];
   const int row0 = blockIdx.x * kKvRows;
   find_rows(c, row0, place);
   __syncthreads();
@@ -99,11 +99,11 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, KvIo io) {
     const int rr = i / (2 * per_side), in = i % (2 * per_side), side = in / per_side;
     const int h = in % per_side / per_head, d = in % per_head * E, r = row0 + rr;
     if (r >= c.rows) break;
-    const long long at = place[rr];
-    const long long src = (at + ((long long)h << c.page_shift)) * c.head_dim + d;
+    const uint32_t at = place[rr];
+    const long long src = (long long)(at + ((uint32_t)h << c.page_shift)) * c.head_dim + d;
     const uint8_t *pool = side ? c.v : c.k;
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (at >= 0) {
+    if (at != kNoRow) {
       if constexpr (F == FMT_F32) {
         u = *(const uint4 *)(pool + 4 * src);
       } else if constexpr (F == FMT_BF16) {

@@ -303,6 +303,26 @@ def test_attention_rows_that_see_nothing(dtype, new):
 
 
 @pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("new", [[1, 2], [80, 40]])
+def test_attention_over_holes_in_the_table(dtype, hd, new):
+    """Entries that are no page in the middle of what a row sees hide their keys;
+    page 0, which stands in for them, is full of NaN."""
+    p = R.Paged(gen(8), new, [1500, 700], 16, 1, hd, dtype)
+    unused = int(p.unused.all(-1).nonzero()[0])
+    swap = p.table == 0
+    p.table[swap] = unused
+    for data, scales in p.pools:
+        data[[0, unused]] = data[[unused, 0]]
+        if scales is not None:
+            scales[[0, unused]] = scales[[unused, 0]]
+    for a in (0, 3, 4, 17, 18, 19, 20, 21, 22, 23, 24, 25, 26, 27, 40):
+        p.table[a % 2, a] = -1
+    p.table[0, 30:47] = p.num_pages + 1
+    check_attention(p, 4)
+
+
+@pytest.mark.parametrize("dtype", CACHES)
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_attention_scales(dtype, scale):
     p = R.Paged(gen(21), [2, 45], [60, 20], 16, 1, 64, dtype)
