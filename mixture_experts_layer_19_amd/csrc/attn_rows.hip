@@ -297,12 +297,14 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
       }
     };
     auto add_not_finite = [&](int k0) MOE_INLINE {
+      int d0 = 4 * g4;
+      asm volatile("" : "+v"(d0));                 // its addresses stay out of the loop's registers
       for (int key = k0; key < k0 + C::keys && key < g.len; ++key) {
         const uint32_t r = pool_row(c, pages[key >> c.page_shift], h, key);
         if (r == kNoRow) continue;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const f32x4 v = not_finite4<F, HD>(c, r, 16 * d + 4 * g4);
+          const f32x4 v = not_finite4<F, HD>(c, r, 16 * d + d0);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
             if (key < hi[rt] && (key >= lo[rt] || key < a.sinks)) o[rt][d] += v;
@@ -403,15 +405,18 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
       const bool inner = all && k0 + C::keys <= all_hi && (k0 >= all_lo || k0 + C::keys <= a.sinks);
       if (!inner) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int kh = 0; kh < NKH; ++kh) {
+          uint32_t bits = there[kh];
+          asm volatile("" : "+v"(bits));           // keeps the masks out of inner tiles
 #pragma unroll
-          for (int kh = 0; kh < NKH; ++kh)
+          for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = 4 * g4 + i, key = k0 + 16 * kh + j;
-              const bool see = ((there[kh] >> j) & 1) && key < hi[rt] && (key >= lo[rt] || key < a.sinks);
+              const bool see = ((bits >> j) & 1) && key < hi[rt] && (key >= lo[rt] || key < a.sinks);
               sc[rt][kh][i] = see ? sc[rt][kh][i] : -INFINITY;
             }
+        }
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {

@@ -23,9 +23,6 @@
 
 namespace moe {
 
-// 16 zero pieces: what a key without a page is read from.
-static __device__ __align__(16) uint4 zero_row[64];
-
 template <int F, int HD, int BK, int QT>
 struct TileCfg {
   static constexpr int rows = 128 * QT;                    // query rows of a workgroup
@@ -33,7 +30,7 @@ struct TileCfg {
   static constexpr int row_bytes = HD * elem, chunks = row_bytes / 16;
   static constexpr int tile = BK * row_bytes;              // K or V
   static constexpr int lds = 4 * tile + 64;
-  // staging, pieces of 16 bytes a thread: bf16 and fp32 by chunk, MX a run of
+  // staging of K or V, pieces of 16 bytes a thread: bf16 and fp32 by chunk, MX a run of
   // HD * BK / 256 codes of one key (under one scale)
   static constexpr int codes = HD * BK / 256;
   static constexpr int pieces = F == FMT_MX8 ? codes / 16 : tile / 16 / 256;
@@ -135,67 +132,60 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 
   // ---- staging
   const int32_t *pages = c.table + (long long)s * c.max_pages;
-  // page of the tile's key `lane` (-1: none)
+  // The table's entry for key `lane` of tile t, and the key's row in the pool.
+  // As in the row kernel no load of the loop stands under a condition: past the
+  // last tile, and for keys without a page, row 0 is read.
   auto page_of = [&](int t) MOE_INLINE {
-    const int key = range.key(t) + (lane & (BK - 1));
-    const int p = key < g.len ? pages[key >> c.page_shift] : -1;
-    return (unsigned)p < (unsigned)c.num_pages ? p : -1;
+    return pages[min((range.key(min(t, t1 - 1)) + (lane & (BK - 1))) >> c.page_shift, c.max_pages - 1)];
   };
-  i32x4 kst[NP], vst[NP];
-  uint32_t kss = 0, vss = 0;
-  auto mx_key = [&]() MOE_INLINE { return tid / (256 / BK); };
-  auto load_tile = [&](int t, int page) MOE_INLINE {
-    const int k0 = range.key(t);
+  auto row_of = [&](int t, int page) MOE_INLINE {
+    const int key = range.key(t) + (lane & (BK - 1));
+    return t < t1 && key < g.len ? pool_row(c, page, h, key) : kNoRow;
+  };
+  // A tile's K or V on its way: K's is stored before V's is loaded, so that
+  // both use the same registers.
+  i32x4 st[NP];
+  uint32_t st_scale = 0;
+  // key of the tile that piece p of this thread belongs to
+  auto piece_key = [&](int p) MOE_INLINE {
+    if constexpr (F == FMT_MX8) return tid / (256 / BK);
+    else return (p * 256 + tid) / C::chunks;
+  };
+  auto load_tile = [&](const uint8_t *pool, const uint8_t *scale, uint32_t row) MOE_INLINE {
+    const uint32_t safe = row == kNoRow ? 0u : row;
     if constexpr (F == FMT_MX8) {
-      const int key = mx_key(), part = tid % (256 / BK);
-      const uint32_t r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
-      const long long at = (long long)(r == kNoRow ? 0 : r) * HD + part * C::codes;
+      const long long at = (long long)__shfl(safe, piece_key(0), 64) * HD + tid % (256 / BK) * C::codes;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        kst[p] = *(const i32x4 *)(c.k + at + 16 * p);
-        vst[p] = *(const i32x4 *)(c.v + at + 16 * p);
-      }
-      kss = c.k_scale[at >> 5];
-      vss = c.v_scale[at >> 5];
-      if (r == kNoRow) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) kst[p] = vst[p] = i32x4{0, 0, 0, 0};
-        kss = vss = 0;
-      }
+      for (int p = 0; p < NP; ++p) st[p] = *(const i32x4 *)(pool + at + 16 * p);
+      st_scale = scale[at >> 5];
     } else {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int id = p * 256 + tid, key = id / C::chunks, ch = id % C::chunks;
-        const uint32_t r = pool_row(c, __shfl(page, key, 64), h, k0 + key);
-        const uint8_t *zero = (const uint8_t *)zero_row;
-        const uint8_t *kp = r == kNoRow ? zero : c.k + (long long)r * C::row_bytes + 16 * ch;
-        const uint8_t *vp = r == kNoRow ? zero : c.v + (long long)r * C::row_bytes + 16 * ch;
-        kst[p] = *(const i32x4 *)kp;
-        vst[p] = *(const i32x4 *)vp;
-      }
+      for (int p = 0; p < NP; ++p)
+        st[p] = *(const i32x4 *)(pool + (long long)__shfl(safe, piece_key(p), 64) * C::row_bytes +
+                                 (p * 256 + tid) % C::chunks * 16);
     }
   };
   // (`finite`: zeros in place of what is not)
-  auto put = [&](uint8_t *tile, const i32x4 (&d)[NP], uint32_t sb, auto finite) MOE_INLINE {
+  auto put = [&](uint8_t *tile, auto finite) MOE_INLINE {
     auto chunk = [&](int key, int ch, uint4 w) MOE_INLINE {
       if constexpr (finite)
         w = make_uint4(word_finite<F>(w.x), word_finite<F>(w.y), word_finite<F>(w.z), word_finite<F>(w.w));
       *(uint4 *)(tile + key * C::row_bytes + ((ch ^ C::swz(key)) << 4)) = w;
     };
     if constexpr (F == FMT_MX8) {
-      const int key = mx_key(), part = tid % (256 / BK);
+      const int key = piece_key(0), part = tid % (256 / BK);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint2 w0 = e4m3_to_bf16x4(d[p][2 * x], sb), w1 = e4m3_to_bf16x4(d[p][2 * x + 1], sb);
+          const uint2 w0 = e4m3_to_bf16x4(st[p][2 * x], st_scale), w1 = e4m3_to_bf16x4(st[p][2 * x + 1], st_scale);
           chunk(key, part * (C::codes / 8) + 2 * p + x, make_uint4(w0.x, w0.y, w1.x, w1.y));
         }
     } else {
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int id = p * 256 + tid;
-        chunk(id / C::chunks, id % C::chunks, __builtin_bit_cast(uint4, d[p]));
+        chunk(id / C::chunks, id % C::chunks, __builtin_bit_cast(uint4, st[p]));
       }
     }
   };
@@ -204,58 +194,84 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
     const int k0 = range.key(t);
     return tok_b > tok_a && (k0 + BK > g.pos0 + tok_a + 1 || (a.window && k0 <= g.pos0 + tok_b - a.window));
   };
-  auto store_tile = [&](int t, int stage) MOE_INLINE {
-    put(lds + 2 * stage * C::tile, kst, kss, std::false_type{});
+  auto store_k = [&](int stage) MOE_INLINE { put(lds + 2 * stage * C::tile, std::false_type{}); };
+  auto store_v = [&](int t, int stage, unsigned long long in) MOE_INLINE {
+    if (in != ~0ull) {                                     // V of keys that do not exist: zeros
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        if (!((in >> piece_key(p)) & 1)) {
+          st[p] = i32x4{0, 0, 0, 0};
+          st_scale = 0;
+        }
+    }
     uint8_t *v = lds + (2 * stage + 1) * C::tile;
     if (partial(t)) {
-      put(v, vst, vss, std::true_type{});
-      bool bad = F == FMT_MX8 && vss >= kScaleOverflow;
+      put(v, std::true_type{});
+      bool bad = F == FMT_MX8 && st_scale >= kScaleOverflow;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad = bad || word_not_finite<F>((uint32_t)vst[p][i]);
+        for (int i = 0; i < 4; ++i) bad = bad || word_not_finite<F>((uint32_t)st[p][i]);
       const unsigned long long any = __ballot(bad);
       if (lane == 0) flags[4 * stage + wave] = any != 0;
     } else {
-      put(v, vst, vss, std::false_type{});
+      put(v, std::false_type{});
     }
   };
 
   // ---- products
   // K: lane q32 reads key row q32 of a 32-key tile, chunk 2 p + hf
-  const int k_addr = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
-  auto scores = [&](const uint8_t *kt_lds, int kt, f32x16 (&sc)[QT]) MOE_INLINE {
+  const uint32_t k_addr = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
+  // V: where this lane's first read lies; the swizzle makes the others' XORs of
+  // it (added to a tile's offset, whose low bits are zero)
+  const uint32_t v_addr =
+      F == FMT_F32 ? 4 * hf * C::row_bytes + (((q32 >> 2) ^ C::swz(4 * hf)) << 4) + 4 * (q32 & 3)
+                   : (4 * hf + ((lane & 15) >> 2)) * C::row_bytes + 8 * (lane & 1) +
+                         (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(4 * hf + ((lane & 15) >> 2))) << 4);
+  auto scores = [&](int stage, f32x16 (&sc)[KT][QT]) MOE_INLINE {
+    uint32_t addr = k_addr + 2 * stage * C::tile;
+    asm volatile("" : "+v"(addr));                       // its XORs are cheaper than registers for them
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sc[qt][i] = 0.0f;
-    const uint8_t *base = kt_lds + 32 * kt * C::row_bytes;
+      for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-    for (int p = 0; p < QP; ++p) {
-      const i32x4 k = *(const i32x4 *)(base + (k_addr ^ (32 * p)));
+        for (int i = 0; i < 16; ++i) sc[kt][qt][i] = 0.0f;
+    static_for<QP>([&](auto p) MOE_INLINE {
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
-        if constexpr (F == FMT_F32) {
+      for (int kt = 0; kt < KT; ++kt) {
+        const i32x4 k = *(const i32x4 *)(lds + (addr ^ (32 * p)) + 32 * kt * C::row_bytes);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sc[qt] = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(k[e]), __int_as_float(q[qt][p][e]),
-                                                          sc[qt], 0, 0, 0);
-        } else {
-          sc[qt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k),
-                                                           __builtin_bit_cast(bf16x8, q[qt][p]), sc[qt], 0, 0, 0);
+        for (int qt = 0; qt < QT; ++qt) {
+          if constexpr (F == FMT_F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[kt][qt] = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(k[e]), __int_as_float(q[qt][p][e]),
+                                                                sc[kt][qt], 0, 0, 0);
+          } else {
+            sc[kt][qt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q[qt][p]), sc[kt][qt], 0, 0, 0);
+          }
         }
       }
-    }
+    });
+    // K's reads run two pieces ahead of the products
+    constexpr int PER = KT * QT * (F == FMT_F32 ? 4 : 1);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * KT, 0);
+    static_for<QP - 2>([&](auto) MOE_INLINE {
+      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, KT, 0);
+    });
+    __builtin_amdgcn_sched_group_barrier(0x008, 2 * PER, 0);
   };
   // O^T += V^T P^T for the 32 columns dt and the 32 keys kt.  The weights of
   // element i are those of key 8 (i / 4) + 4 hf + i % 4.
-  auto add_pv = [&](const uint8_t *v_lds, int kt, int dt, const f32x16 (&p)[QT], const i32x4 (&pw)[QT][2]) MOE_INLINE {
+  auto add_pv = [&](uint32_t addr, int kt, int dt, const f32x16 (&p)[QT], const i32x4 (&pw)[QT][2]) MOE_INLINE {
     if constexpr (F == FMT_F32) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int key = 32 * kt + 8 * (i / 4) + 4 * hf + i % 4;
-        const int ch = (8 * dt + (q32 >> 2)) ^ C::swz(key);
-        const float v = *(const float *)(v_lds + key * C::row_bytes + (ch << 4) + 4 * (q32 & 3));
+        const float v = *(const float *)(lds + (addr ^ (16 * (i % 4)) ^ (128 * dt)) +
+                                         (32 * kt + 8 * (i / 4) + i % 4) * C::row_bytes);
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt)
           o[qt][dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[qt][i], o[qt][dt], 0, 0, 0);
@@ -267,11 +283,9 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           // a group of 16 lanes reads 4 keys x 16 columns, transposed
-          const int key = 32 * kt + 16 * st + 8 * b + 4 * hf + ((lane & 15) >> 2);
-          const int ch = (4 * dt + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(key);
           using lds_s16x4 = __attribute__((address_space(3))) s16x4;
           v[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4 *)(v_lds + key * C::row_bytes + (ch << 4) + 8 * (lane & 1)));
+              (lds_s16x4 *)(lds + (addr ^ (64 * dt) ^ (32 * b)) + (32 * kt + 16 * st + 8 * b) * C::row_bytes));
         }
         const auto vv = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
@@ -283,6 +297,8 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
   };
 
   auto add_not_finite = [&](int k0) MOE_INLINE {
+    int d0 = 4 * hf;
+    asm volatile("" : "+v"(d0));                   // its addresses stay out of the loop's registers
     for (int key = k0; key < k0 + BK && key < g.len; ++key) {
       const uint32_t r = pool_row(c, pages[key >> c.page_shift], h, key);
       if (r == kNoRow) continue;
@@ -290,7 +306,7 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const f32x4 v = not_finite4<F, HD>(c, r, 32 * d + 8 * b + 4 * hf);
+          const f32x4 v = not_finite4<F, HD>(c, r, 32 * d + 8 * b + d0);
 #pragma unroll
           for (int qt = 0; qt < QT; ++qt)
             if (key < hi[qt] && (key >= lo[qt] || key < a.sinks))
@@ -301,37 +317,46 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
   };
 
   if (t0 < t1) {
-    int page = page_of(t0);
-    unsigned long long there = __ballot(page >= 0);
-    load_tile(t0, page);
-    page = t0 + 1 < t1 ? page_of(t0 + 1) : -1;
-    store_tile(t0, 0);
+    uint32_t row = row_of(t0, page_of(t0));
+    unsigned long long there = __ballot(row != kNoRow);
+    load_tile(c.k, c.k_scale, row);
+    store_k(0);
+    load_tile(c.v, c.v_scale, row);
+    int page = page_of(t0 + 1);
+    store_v(t0, 0, there);
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
       const int stage = (t - t0) & 1, k0 = range.key(t);
-      const bool more = t + 1 < t1;
-      const uint8_t *kl = lds + 2 * stage * C::tile, *vl = kl + C::tile;
       const unsigned long long there_now = there;
-      if (more) {
-        load_tile(t + 1, page);
-        there = __ballot(page >= 0);
-        if (t + 2 < t1) page = page_of(t + 2);
-      }
+      row = row_of(t + 1, page);
+      there = __ballot(row != kNoRow);
+      load_tile(c.k, c.k_scale, row);
+      __builtin_amdgcn_sched_barrier(0);
       const bool seen = has_rows && k0 < any_hi && (k0 + BK > any_lo || k0 < a.sinks);
       const bool inner = k0 + BK <= all_hi && (k0 >= all_lo || k0 + BK <= a.sinks) && there_now == ~0ull;
+      f32x16 sc[KT][QT];
+      if (seen) scores(stage, sc);
+      __builtin_amdgcn_sched_barrier(0);
+      store_k(stage ^ 1);
+      load_tile(c.v, c.v_scale, row);
+      page = page_of(t + 2);
+      __builtin_amdgcn_sched_barrier(0);
       if (seen) {
-        f32x16 sc[KT][QT];
-        static_for<KT>([&](auto kt) MOE_INLINE { scores(kl, kt, sc[kt]); });
         if (!inner) {
           static_for<KT>([&](auto kt) MOE_INLINE {
+            uint32_t bits = (uint32_t)(there_now >> (32 * kt)) >> (4 * hf);
+            asm volatile("" : "+v"(bits));                 // keeps the masks out of inner tiles
+            const int base = k0 + 32 * kt + 4 * hf;
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
+            for (int qt = 0; qt < QT; ++qt) {
+              const int below = hi[qt] - base, from = lo[qt] - base, sink = a.sinks - base;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const int j = 32 * kt + 8 * (i / 4) + 4 * hf + i % 4, key = k0 + j;
-                const bool see = ((there_now >> j) & 1) && key < hi[qt] && (key >= lo[qt] || key < a.sinks);
+                const int j = 8 * (i / 4) + i % 4;
+                const bool see = ((bits >> j) & 1) && j < below && (j >= from || j < sink);
                 sc[kt][qt][i] = see ? sc[kt][qt][i] : -INFINITY;
               }
+            }
           });
         }
         i32x4 pw[KT][QT][2];
@@ -372,13 +397,15 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
           }
           sum[qt] += part;
         }
+        uint32_t addr = v_addr + (2 * stage + 1) * C::tile;
+        asm volatile("" : "+v"(addr));
         static_for<KT>([&](auto kt) MOE_INLINE {
-          static_for<DT>([&](auto dt) MOE_INLINE { add_pv(vl, kt, dt, sc[kt], pw[kt]); });
+          static_for<DT>([&](auto dt) MOE_INLINE { add_pv(addr, kt, dt, sc[kt], pw[kt]); });
         });
         if (partial(t) && (flags[4 * stage] | flags[4 * stage + 1] | flags[4 * stage + 2] | flags[4 * stage + 3]))
           add_not_finite(k0);
       }
-      if (more) store_tile(t + 1, stage ^ 1);
+      if (t + 1 < t1) store_v(t + 1, stage ^ 1, there);
       __syncthreads();
     }
   }

@@ -108,9 +108,9 @@ __device__ __forceinline__ int seq_of_row(const KvArgs &c, int r) {
 // than 2^32 - 1 rows.)
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t pool_row(const KvArgs &c, int page, int head, int key) {
-  if ((unsigned)page >= (unsigned)c.num_pages) return kNoRow;
-  return (((uint32_t)page * (uint32_t)c.kv_heads + (uint32_t)head) << c.page_shift) |
-         ((uint32_t)key & ((1u << c.page_shift) - 1u));
+  const uint32_t row = (((uint32_t)page * (uint32_t)c.kv_heads + (uint32_t)head) << c.page_shift) |
+                       ((uint32_t)key & ((1u << c.page_shift) - 1u));
+  return (unsigned)page < (unsigned)c.num_pages ? row : kNoRow;
 }
 
 }  // namespace moe
