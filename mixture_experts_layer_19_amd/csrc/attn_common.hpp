@@ -92,7 +92,8 @@ __device__ __forceinline__ void clear_free_rows(const AttnArgs &a) {
   const int first = min(max(c.offsets[0], 0), c.rows), last = min(max(c.offsets[c.seqs], 0), c.rows);
   if (first == 0 && last == c.rows) return;
   const long long per_row = (long long)a.heads * HD * (F == FMT_F32 ? 4 : 2) / 16;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < c.rows * per_row; i += gridDim.x * 256ll) {
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < c.rows * per_row;
+       i += (long long)gridDim.x * blockDim.x) {
     const long long r = i / per_row;
     if (r < first || r >= last) ((uint4 *)a.out)[i] = make_uint4(0, 0, 0, 0);
   }

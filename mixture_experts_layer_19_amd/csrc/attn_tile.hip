@@ -1,18 +1,22 @@
 // attn_tile.hip -- attention of chunks of new tokens over the paged cache.
 //
 // Bound by the matrix cores (bf16: 4 head_dim flops a row and key) and, next
-// to them, by the LDS that feeds them and the exponentials.  A workgroup of
-// four waves takes 128 QT query rows (tokens x heads of the group) and walks
-// the keys in tiles of BK; a wave owns 32 QT rows.  S^T = K Q^T and
-// O^T = V^T P^T on 32x32 matrix instructions: a lane holds scores of one query
-// only, so the running maximum and sum are per lane (one exchange between the
-// half waves), rescaling needs no other lane, and the weights are already the
-// operand that the second product reads.
+// to them, by the exponentials and the LDS that feeds them.  A workgroup of
+// NW waves takes 32 NW query rows (tokens x heads of the group) and walks the
+// keys in tiles of 64; a wave owns 32 rows.  S^T = K Q^T and O^T = V^T P^T on
+// 32x32 matrix instructions: a lane holds scores of one query only, so the
+// running maximum and sum are per lane (one exchange between the half waves),
+// rescaling needs no other lane, and the weights are already the operand that
+// the second product reads.
+//
+// The loop is a pipeline over halves of a tile: while the softmax of one half
+// runs on the vector units, the matrix cores work on the scores of the next
+// and the values of the last (step, below).
 //
 // K and V tiles come through registers (MX codes become bf16 there, exactly)
-// into two LDS buffers: the loads of tile t + 1 run under the products of
-// tile t, one barrier a tile.  Rows are XOR-swizzled in 16-byte chunks so that
-// both reads, K's by rows and V's transposed, spread over the banks.
+// into two LDS buffers each, with one barrier a tile.  Rows are XOR-swizzled in
+// 16-byte chunks so that both reads, K's by rows and V's transposed, spread
+// over the banks (no conflicts counted).
 //
 // The running maximum is a reference that moves only when a score passes it
 // by 2^8: the weights stay below 2^8 of fp32 and the output is rescaled rarely.
@@ -23,19 +27,21 @@
 
 namespace moe {
 
-template <int F, int HD, int BK, int QT>
+template <int F, int HD, int NW>
 struct TileCfg {
-  static constexpr int rows = 128 * QT;                    // query rows of a workgroup
+  static constexpr int threads = 64 * NW, rows = 32 * NW;  // query rows of a workgroup
+  static constexpr int BK = 64;                            // keys of a tile
   static constexpr int elem = F == FMT_F32 ? 4 : 2;        // in LDS
   static constexpr int row_bytes = HD * elem, chunks = row_bytes / 16;
   static constexpr int tile = BK * row_bytes;              // K or V
-  static constexpr int lds = 4 * tile + 64;
-  // staging of K or V, pieces of 16 bytes a thread: bf16 and fp32 by chunk, MX a run of
-  // HD * BK / 256 codes of one key (under one scale)
-  static constexpr int codes = HD * BK / 256;
-  static constexpr int pieces = F == FMT_MX8 ? codes / 16 : tile / 16 / 256;
+  static constexpr int lds = 4 * tile + 8 * NW;
+  // staging of K or V, pieces of 16 bytes a thread: bf16 and fp32 by chunk, MX
+  // 16 codes or more of one key (parts threads a key; threads beyond them do
+  // what others do)
+  static constexpr int parts = HD / 16 < NW ? HD / 16 : NW, codes = HD / parts, scales = codes > 32 ? codes / 32 : 1;
+  static constexpr int pieces = F == FMT_MX8 ? codes / 16 : tile / 16 / threads;
   static constexpr int QP = row_bytes / 32;                // 16-byte query pieces a lane
-  static constexpr int KT = BK / 32, DT = HD / 32;
+  static constexpr int DT = HD / 32;
   // chunk c of key row r is stored at chunk c ^ swz(r)
   __device__ __forceinline__ static int swz(int r) {
     if constexpr (F == FMT_F32) return (r & 7) ^ (((r >> 2) & 1) << 3);
@@ -44,18 +50,31 @@ struct TileCfg {
   }
 };
 
-// Sequence and row tile of unit u, or s = -1 past the last unit.  The row
-// tiles of a sequence come longest first.
+// Sequence and row tile of unit u, or s = -1 past the last unit.  Long units
+// come first, so that the last ones to start are short: of each 64 sequences
+// the longest first, the row tiles of a sequence from its end.
 template <int ROWS>
 __device__ __forceinline__ void find_unit(const AttnArgs &a, int u, int &s, int &rt) {
   const int lane = threadIdx.x & 63;
   s = -1;
   rt = 0;
   for (int s0 = 0; s0 < a.c.seqs; s0 += 64) {
-    int own = 0;
-    if (s0 + lane < a.c.seqs)
-      own = (int)(((long long)seq_geo(a.c, s0 + lane).n * a.group + ROWS - 1) / ROWS);
-    int v = own;
+    int units = 0, len = -1;
+    if (s0 + lane < a.c.seqs) {
+      const SeqGeo g = seq_geo(a.c, s0 + lane);
+      units = (int)(((long long)g.n * a.group + ROWS - 1) / ROWS);
+      len = g.len;
+    }
+    const int n = min(a.c.seqs - s0, 64);
+    int rank = 0;                                  // sequences before this one
+    for (int i = 0; i < n; ++i) {
+      const int other = __builtin_amdgcn_readlane(len, i);
+      rank += other > len || (other == len && i < lane);
+    }
+    if (lane >= n) rank = lane;
+    // lane r: the sequence of rank r
+    const int seq = __builtin_amdgcn_ds_permute(rank << 2, lane);
+    int v = __shfl(units, seq, 64);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int w = __shfl_up(v, d, 64);
@@ -64,7 +83,7 @@ __device__ __forceinline__ void find_unit(const AttnArgs &a, int u, int &s, int 
     const unsigned long long past = __ballot(v > u);
     if (past) {
       const int l = __ffsll((long long)past) - 1;
-      s = s0 + l;
+      s = s0 + __shfl(seq, l, 64);
       rt = __shfl(v, l, 64) - 1 - u;               // descending
       return;
     }
@@ -72,10 +91,10 @@ __device__ __forceinline__ void find_unit(const AttnArgs &a, int u, int &s, int 
   }
 }
 
-template <int F, int HD, int BK, int QT, int OCC>
-__global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int splits) {
-  using C = TileCfg<F, HD, BK, QT>;
-  constexpr int ROWS = C::rows, KT = C::KT, DT = C::DT, QP = C::QP, NP = C::pieces;
+template <int F, int HD, int NW, int OCC>
+__global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int splits) {
+  using C = TileCfg<F, HD, NW>;
+  constexpr int ROWS = C::rows, BK = C::BK, DT = C::DT, QP = C::QP, NP = C::pieces;
   extern __shared__ __align__(16) uint8_t lds[];           // K0 V0 K1 V1, flags
   int *flags = (int *)(lds + 4 * C::tile);                 // [stage][wave]
   const int tid = threadIdx.x, lane = tid & 63, q32 = lane & 31, hf = lane >> 5;
@@ -95,40 +114,28 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
   const int per = (range.tiles + splits - 1) / splits;
   const int t0 = min(split * per, range.tiles), t1 = min(t0 + per, range.tiles);
 
-  // queries: lane q32 holds row rt0 + 32 (QT wave + qt) + q32
-  i32x4 q[QT][QP];
-  int lo[QT], hi[QT];
-  const int m0 = rt0 + 32 * QT * wave;
-  static_for<QT>([&](auto qt) MOE_INLINE {
-    const int m = m0 + 32 * qt + q32;
-    const bool in = m < nrows;
-    const int tok = in ? m / a.group : 0, hq = h * a.group + (in ? m % a.group : 0);
+  // query: lane q32 holds row m
+  i32x4 q[QP];
+  const int m0 = rt0 + 32 * wave, m = m0 + q32;
+  const bool in = m < nrows, has_rows = m0 < nrows;
+  const int own_tok = in ? m / a.group : 0, hq = h * a.group + (in ? m % a.group : 0);
+  {
     const uint8_t *qp =
-        (const uint8_t *)a.q + ((long long)(g.r0 + tok) * a.q_row + hq * a.q_head) * C::elem + 16 * hf;
+        (const uint8_t *)a.q + ((long long)(g.r0 + own_tok) * a.q_row + hq * a.q_head) * C::elem + 16 * hf;
 #pragma unroll
-    for (int p = 0; p < QP; ++p) q[qt][p] = in ? *(const i32x4 *)(qp + 32 * p) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
-    const RowMask mask(g, tok, in, a.window, a.sinks);
-    hi[qt] = mask.hi;
-    lo[qt] = mask.lo;
-  });
-  // the wave's tokens; the keys that all, and that any, of its rows see
-  const int wtok_a = m0 / a.group, wtok_b = (min(m0 + 32 * QT, nrows) - 1) / a.group;
-  const bool has_rows = m0 < nrows;
-  const int all_hi = min(g.pos0 + wtok_a + 1, g.len), any_hi = min(g.pos0 + wtok_b + 1, g.len);
-  const int all_lo = a.window ? g.pos0 + wtok_b - a.window + 1 : 0;
-  const int any_lo = a.window ? g.pos0 + wtok_a - a.window + 1 : 0;
-
-  f32x16 o[QT][DT];
-  float mx[QT], sum[QT];
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    mx[qt] = kNegBig;
-    sum[qt] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[qt][d][i] = 0.0f;
+    for (int p = 0; p < QP; ++p) q[p] = in ? *(const i32x4 *)(qp + 32 * p) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
   }
+  const RowMask mask(g, own_tok, in, a.window, a.sinks);
+  // the wave's tokens, and the keys that all of them see
+  const int wtok_a = m0 / a.group, wtok_b = (min(m0 + 32, nrows) - 1) / a.group;
+  const int all_hi = min(g.pos0 + wtok_a + 1, g.len), all_lo = a.window ? g.pos0 + wtok_b - a.window + 1 : 0;
+
+  f32x16 o[DT];
+  float mx = kNegBig, sum = 0.0f;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
   // ---- staging
   const int32_t *pages = c.table + (long long)s * c.max_pages;
@@ -136,57 +143,56 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
   // As in the row kernel no load of the loop stands under a condition: past the
   // last tile, and for keys without a page, row 0 is read.
   auto page_of = [&](int t) MOE_INLINE {
-    return pages[min((range.key(min(t, t1 - 1)) + (lane & (BK - 1))) >> c.page_shift, c.max_pages - 1)];
+    return pages[min((range.key(min(t, t1 - 1)) + lane) >> c.page_shift, c.max_pages - 1)];
   };
   auto row_of = [&](int t, int page) MOE_INLINE {
-    const int key = range.key(t) + (lane & (BK - 1));
+    const int key = range.key(t) + lane;
     return t < t1 && key < g.len ? pool_row(c, page, h, key) : kNoRow;
   };
-  // A tile's K or V on its way: K's is stored before V's is loaded, so that
-  // both use the same registers.
-  i32x4 st[NP];
-  uint32_t st_scale = 0;
+  // a tile's K or V on its way
+  struct Stage {
+    i32x4 d[NP];
+    uint32_t scale[C::scales];
+  };
   // key of the tile that piece p of this thread belongs to
   auto piece_key = [&](int p) MOE_INLINE {
-    if constexpr (F == FMT_MX8) return tid / (256 / BK);
-    else return (p * 256 + tid) / C::chunks;
+    if constexpr (F == FMT_MX8) return tid / C::parts % BK;
+    else return (p * C::threads + tid) / C::chunks;
   };
-  auto load_tile = [&](const uint8_t *pool, const uint8_t *scale, uint32_t row) MOE_INLINE {
+  auto load_tile = [&](Stage &st, const uint8_t *pool, const uint8_t *scale, uint32_t row) MOE_INLINE {
     const uint32_t safe = row == kNoRow ? 0u : row;
     if constexpr (F == FMT_MX8) {
-      const long long at = (long long)__shfl(safe, piece_key(0), 64) * HD + tid % (256 / BK) * C::codes;
+      const long long at = (long long)__shfl(safe, piece_key(0), 64) * HD + tid % C::parts * C::codes;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) st[p] = *(const i32x4 *)(pool + at + 16 * p);
-      st_scale = scale[at >> 5];
+      for (int p = 0; p < NP; ++p) st.d[p] = *(const i32x4 *)(pool + at + 16 * p);
+#pragma unroll
+      for (int i = 0; i < C::scales; ++i) st.scale[i] = scale[(at >> 5) + i];
     } else {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        st[p] = *(const i32x4 *)(pool + (long long)__shfl(safe, piece_key(p), 64) * C::row_bytes +
-                                 (p * 256 + tid) % C::chunks * 16);
+        st.d[p] = *(const i32x4 *)(pool + (long long)__shfl(safe, piece_key(p), 64) * C::row_bytes +
+                                   (p * C::threads + tid) % C::chunks * 16);
     }
   };
   // (`finite`: zeros in place of what is not)
-  auto put = [&](uint8_t *tile, auto finite) MOE_INLINE {
+  auto put = [&](const Stage &st, uint8_t *tile, auto finite) MOE_INLINE {
     auto chunk = [&](int key, int ch, uint4 w) MOE_INLINE {
       if constexpr (finite)
         w = make_uint4(word_finite<F>(w.x), word_finite<F>(w.y), word_finite<F>(w.z), word_finite<F>(w.w));
       *(uint4 *)(tile + key * C::row_bytes + ((ch ^ C::swz(key)) << 4)) = w;
     };
     if constexpr (F == FMT_MX8) {
-      const int key = piece_key(0), part = tid % (256 / BK);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint2 w0 = e4m3_to_bf16x4(st[p][2 * x], st_scale), w1 = e4m3_to_bf16x4(st[p][2 * x + 1], st_scale);
-          chunk(key, part * (C::codes / 8) + 2 * p + x, make_uint4(w0.x, w0.y, w1.x, w1.y));
+          const uint32_t sb = st.scale[p * 16 / 32 % C::scales];
+          const uint2 w0 = e4m3_to_bf16x4(st.d[p][2 * x], sb), w1 = e4m3_to_bf16x4(st.d[p][2 * x + 1], sb);
+          chunk(piece_key(0), tid % C::parts * (C::codes / 8) + 2 * p + x, make_uint4(w0.x, w0.y, w1.x, w1.y));
         }
     } else {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int id = p * 256 + tid;
-        chunk(id / C::chunks, id % C::chunks, __builtin_bit_cast(uint4, st[p]));
-      }
+      for (int p = 0; p < NP; ++p) chunk(piece_key(p), (p * C::threads + tid) % C::chunks, __builtin_bit_cast(uint4, st.d[p]));
     }
   };
   // Tiles in which some of the workgroup's rows see a key that others do not.
@@ -194,112 +200,117 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
     const int k0 = range.key(t);
     return tok_b > tok_a && (k0 + BK > g.pos0 + tok_a + 1 || (a.window && k0 <= g.pos0 + tok_b - a.window));
   };
-  auto store_k = [&](int stage) MOE_INLINE { put(lds + 2 * stage * C::tile, std::false_type{}); };
-  auto store_v = [&](int t, int stage, unsigned long long in) MOE_INLINE {
-    if (in != ~0ull) {                                     // V of keys that do not exist: zeros
+  auto k_tile = [&](int t) MOE_INLINE { return lds + 2 * ((t - t0) & 1) * C::tile; };
+  auto v_tile = [&](int t) MOE_INLINE { return lds + (2 * ((t - t0) & 1) + 1) * C::tile; };
+  auto store_v = [&](Stage &st, int t, unsigned long long have) MOE_INLINE {
+    if (have != ~0ull) {                                   // V of keys that do not exist: zeros
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        if (!((in >> piece_key(p)) & 1)) {
-          st[p] = i32x4{0, 0, 0, 0};
-          st_scale = 0;
+        if (!((have >> piece_key(p)) & 1)) {
+          st.d[p] = i32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < C::scales; ++i) st.scale[i] = 0;
         }
     }
-    uint8_t *v = lds + (2 * stage + 1) * C::tile;
     if (partial(t)) {
-      put(v, std::true_type{});
-      bool bad = F == FMT_MX8 && st_scale >= kScaleOverflow;
+      put(st, v_tile(t), std::true_type{});
+      bool bad = false;
+      if constexpr (F == FMT_MX8)
+#pragma unroll
+        for (int i = 0; i < C::scales; ++i) bad = bad || st.scale[i] >= kScaleOverflow;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad = bad || word_not_finite<F>((uint32_t)st[p][i]);
+        for (int i = 0; i < 4; ++i) bad = bad || word_not_finite<F>((uint32_t)st.d[p][i]);
       const unsigned long long any = __ballot(bad);
-      if (lane == 0) flags[4 * stage + wave] = any != 0;
+      if (lane == 0) flags[NW * ((t - t0) & 1) + wave] = any != 0;
     } else {
-      put(v, std::false_type{});
+      put(st, v_tile(t), std::false_type{});
     }
   };
 
-  // ---- products
-  // K: lane q32 reads key row q32 of a 32-key tile, chunk 2 p + hf
+  // ---- products, of halves of a tile (32 keys).  Addresses within LDS: the
+  // swizzle makes all of a lane's reads XORs and offsets of its first; they are
+  // made anew from an opaque copy, which is cheaper than registers for them.
+  // K: lane q32 reads key row q32 of a half, chunk 2 p + hf
   const uint32_t k_addr = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
-  // V: where this lane's first read lies; the swizzle makes the others' XORs of
-  // it (added to a tile's offset, whose low bits are zero)
   const uint32_t v_addr =
       F == FMT_F32 ? 4 * hf * C::row_bytes + (((q32 >> 2) ^ C::swz(4 * hf)) << 4) + 4 * (q32 & 3)
                    : (4 * hf + ((lane & 15) >> 2)) * C::row_bytes + 8 * (lane & 1) +
                          (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(4 * hf + ((lane & 15) >> 2))) << 4);
-  auto scores = [&](int stage, f32x16 (&sc)[KT][QT]) MOE_INLINE {
-    uint32_t addr = k_addr + 2 * stage * C::tile;
-    asm volatile("" : "+v"(addr));                       // its XORs are cheaper than registers for them
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sc[kt][qt][i] = 0.0f;
-    static_for<QP>([&](auto p) MOE_INLINE {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const i32x4 k = *(const i32x4 *)(lds + (addr ^ (32 * p)) + 32 * kt * C::row_bytes);
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-          if constexpr (F == FMT_F32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[kt][qt] = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(k[e]), __int_as_float(q[qt][p][e]),
-                                                                sc[kt][qt], 0, 0, 0);
-          } else {
-            sc[kt][qt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q[qt][p]), sc[kt][qt], 0, 0, 0);
-          }
-        }
-      }
-    });
-    // K's reads run two pieces ahead of the products
-    constexpr int PER = KT * QT * (F == FMT_F32 ? 4 : 1);
-    __builtin_amdgcn_sched_group_barrier(0x100, 2 * KT, 0);
-    static_for<QP - 2>([&](auto) MOE_INLINE {
-      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, KT, 0);
-    });
-    __builtin_amdgcn_sched_group_barrier(0x008, 2 * PER, 0);
+  // The products of a step, in slots: even ones a piece of the scores' head_dim
+  // (S^T; element i is key 8 (i / 4) + 4 hf + i % 4 of the half), odd ones 16
+  // keys (fp32: 4) of the values for 32 columns.  So neighbours do not wait for
+  // each other's sums.
+  constexpr int PV = F == FMT_F32 ? 4 : 2, SLOTS = QP + PV * DT;
+  static_assert(QP == PV * DT, "as many pieces of scores as of values");
+  // the softmax weights of a half: fp32, or bf16 in pairs
+  using Weights = std::conditional_t<F == FMT_F32, f32x16, i32x8>;
+  auto read_k = [&](uint32_t addr, auto n, int half) MOE_INLINE {
+    return *(const i32x4 *)(lds + (addr ^ (32 * n)) + 32 * half * C::row_bytes);
   };
-  // O^T += V^T P^T for the 32 columns dt and the 32 keys kt.  The weights of
-  // element i are those of key 8 (i / 4) + 4 hf + i % 4.
-  auto add_pv = [&](uint32_t addr, int kt, int dt, const f32x16 (&p)[QT], const i32x4 (&pw)[QT][2]) MOE_INLINE {
+  auto read_v = [&](uint32_t addr, auto n, int half) MOE_INLINE {
+    constexpr int dt = n % DT, part = n / DT;
+    i32x4 f;
     if constexpr (F == FMT_F32) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = *(const float *)(lds + (addr ^ (16 * (i % 4)) ^ (128 * dt)) +
-                                         (32 * kt + 8 * (i / 4) + i % 4) * C::row_bytes);
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
-          o[qt][dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[qt][i], o[qt][dt], 0, 0, 0);
-      }
+      for (int i = 0; i < 4; ++i)
+        f[i] = *(const int *)(lds + (addr ^ (16 * i) ^ (128 * dt)) + (32 * half + 8 * part + i) * C::row_bytes);
     } else {
+      using lds_i32x2 = __attribute__((address_space(3))) s16x4;
+      // a group of 16 lanes reads 4 keys x 16 columns, transposed
+      const i32x2 v0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i32x2 *)(
+          lds + (addr ^ (64 * dt)) + (32 * half + 16 * part) * C::row_bytes)));
+      const i32x2 v1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i32x2 *)(
+          lds + (addr ^ (64 * dt) ^ 32) + (32 * half + 16 * part + 8) * C::row_bytes)));
+      f = __builtin_shufflevector(v0, v1, 0, 1, 2, 3);
+    }
+    return f;
+  };
+  auto mul_k = [&](f32x16 &sc, const i32x4 &k, auto n) MOE_INLINE {
+    if constexpr (F == FMT_F32) {
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        s16x4 v[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          // a group of 16 lanes reads 4 keys x 16 columns, transposed
-          using lds_s16x4 = __attribute__((address_space(3))) s16x4;
-          v[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4 *)(lds + (addr ^ (64 * dt) ^ (32 * b)) + (32 * kt + 16 * st + 8 * b) * C::row_bytes));
-        }
-        const auto vv = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
-          o[qt][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv),
-                                                             __builtin_bit_cast(bf16x8, pw[qt][st]), o[qt][dt], 0, 0, 0);
-      }
+      for (int e = 0; e < 4; ++e)
+        sc = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(k[e]), __int_as_float(q[n][e]), sc, 0, 0, 0);
+    } else {
+      sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q[n]), sc,
+                                                   0, 0, 0);
     }
   };
-
-  auto add_not_finite = [&](int k0) MOE_INLINE {
+  auto mul_v = [&](const Weights &w, const i32x4 &v, auto n) MOE_INLINE {
+    constexpr int dt = n % DT, part = n / DT;
+    if constexpr (F == FMT_F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(v[i]), w[4 * part + i], o[dt], 0, 0, 0);
+    } else {
+      const i32x4 pw = {w[4 * part], w[4 * part + 1], w[4 * part + 2], w[4 * part + 3]};
+      o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, pw),
+                                                     o[dt], 0, 0, 0);
+    }
+  };
+  auto k_from = [&](int t) MOE_INLINE {
+    uint32_t addr = k_addr + (uint32_t)(k_tile(t) - lds);
+    asm volatile("" : "+v"(addr));
+    return addr;
+  };
+  auto v_from = [&](int t) MOE_INLINE {
+    uint32_t addr = v_addr + (uint32_t)(v_tile(t) - lds);
+    asm volatile("" : "+v"(addr));
+    return addr;
+  };
+  // what is not finite of V in half `half` of a partial tile (zeros in LDS)
+  auto add_not_finite = [&](int t, int half) MOE_INLINE {
+    const int *f = flags + NW * ((t - t0) & 1);
+    if (!partial(t)) return;
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) any |= f[i];
+    if (!any) return;
     int d0 = 4 * hf;
     asm volatile("" : "+v"(d0));                   // its addresses stay out of the loop's registers
-    for (int key = k0; key < k0 + BK && key < g.len; ++key) {
+    const int k0 = range.key(t) + 32 * half;
+    for (int key = k0; key < k0 + 32 && key < g.len; ++key) {
       const uint32_t r = pool_row(c, pages[key >> c.page_shift], h, key);
       if (r == kNoRow) continue;
 #pragma unroll
@@ -307,142 +318,174 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const f32x4 v = not_finite4<F, HD>(c, r, 32 * d + 8 * b + d0);
+          if (mask.sees(key))
 #pragma unroll
-          for (int qt = 0; qt < QT; ++qt)
-            if (key < hi[qt] && (key >= lo[qt] || key < a.sinks))
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[qt][d][4 * b + i] += v[i];
+            for (int i = 0; i < 4; ++i) o[d][4 * b + i] += v[i];
         }
+    }
+  };
+  // One half: cur holds its scores and becomes the weights w; meanwhile the
+  // next half's scores go to next, and the last half's weights last multiply
+  // its values.  The three do not depend on each other, so the matrix cores run
+  // under the softmax of the same wave.
+  //   half 0: next = half 1 of tile t, last = half 1 of tile t - 1
+  //   half 1: next = half 0 of tile t + 1, last = half 0 of tile t
+  auto step = [&](auto half, int t, unsigned long long have, f32x16 &cur, f32x16 &next, Weights &w,
+                  const Weights &last) MOE_INLINE {
+    const int k0 = range.key(t) + 32 * half;
+    const uint32_t have32 = (uint32_t)(have >> (32 * half));
+    const bool inner = k0 + 32 <= all_hi && (k0 >= all_lo || k0 + 32 <= a.sinks) && have32 == ~0u;
+    if (!inner) {
+      uint32_t bits = have32 >> (4 * hf);
+      asm volatile("" : "+v"(bits));               // keeps the masks out of inner halves
+      const int base = k0 + 4 * hf, below = mask.hi - base, from = mask.lo - base, sink = a.sinks - base;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = 8 * (i / 4) + i % 4;
+        const bool see = ((bits >> j) & 1) && j < below && (j >= from || j < sink);
+        cur[i] = see ? cur[i] : -INFINITY;
+      }
+    }
+    // Slots in this order, the reads AHEAD slots before their product.  The
+    // maximum comes first, the exponentials are spread over the slots, and
+    // their sum and rounding follow one slot behind.
+    constexpr int AHEAD = 4, FIRST = 2, SPAN = SLOTS - FIRST - 1;
+    const uint32_t ka = k_from(half ? t + 1 : t), va = v_from(half ? t : t - 1);
+    i32x4 frag[AHEAD];
+    auto read = [&](auto n) MOE_INLINE {
+      if constexpr (n % 2) frag[n % AHEAD] = read_v(va, std::integral_constant<int, n / 2>{}, 1 - half);
+      else frag[n % AHEAD] = read_k(ka, std::integral_constant<int, n / 2>{}, 1 - half);
+    };
+    static_for<AHEAD>([&](auto n) MOE_INLINE { read(n); });
+    __builtin_amdgcn_sched_barrier(0);
+    float top = -INFINITY, now = 0.0f, alpha = 0.0f, part[2] = {0.0f, 0.0f};
+    static_for<SLOTS>([&](auto n) MOE_INLINE {
+      if constexpr (n == 0)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) next[i] = 0.0f;
+      if constexpr (n % 2) mul_v(last, frag[n % AHEAD], std::integral_constant<int, n / 2>{});
+      else mul_k(next, frag[n % AHEAD], std::integral_constant<int, n / 2>{});
+      if constexpr (n + AHEAD < SLOTS) read(std::integral_constant<int, n + AHEAD>{});
+      if constexpr (n == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, cur[i]);
+      }
+      if constexpr (n == 1) {
+        top = max_half(top) * a.scale;             // the scale is positive
+        // the reference moves only when a score passes it by 2^8
+        now = top > mx + 8.0f ? top : mx;
+        alpha = __builtin_amdgcn_exp2f(mx - now);
+      }
+      // elements whose exponentials are due in slot n: [due(n), due(n + 1))
+      auto due = [](int m) constexpr { return m <= FIRST ? 0 : m >= FIRST + SPAN ? 16 : 16 * (m - FIRST) / SPAN; };
+      constexpr int e0 = due(n), e1 = due(n + 1), d0 = due(n - 1);
+#pragma unroll
+      for (int i = e0; i < e1; ++i) cur[i] = __builtin_amdgcn_exp2f(fmaf(cur[i], a.scale, -now));
+#pragma unroll
+      for (int i = d0; i < e0; ++i) {
+        part[i % 2] += cur[i];
+        if constexpr (F != FMT_F32)
+          if (i % 2) w[i / 2] = (int)bf16_pack2(cur[i - 1], cur[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (F == FMT_F32) w = cur;
+    sum = fmaf(sum, alpha, part[0] + part[1]);
+    asm volatile("" : "+v"(w), "+v"(sum));         // ahead of the branches below
+    add_not_finite(half ? t : t - 1, 1 - half);
+    const bool moved = now > mx;
+    mx = now;
+    if (__ballot(moved)) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
     }
   };
 
   if (t0 < t1) {
-    uint32_t row = row_of(t0, page_of(t0));
-    unsigned long long there = __ballot(row != kNoRow);
-    load_tile(c.k, c.k_scale, row);
-    store_k(0);
-    load_tile(c.v, c.v_scale, row);
-    int page = page_of(t0 + 1);
-    store_v(t0, 0, there);
+    // Ahead of the loop: K of two tiles, V of one, zeros for the values of the
+    // half before the first (whose weights are zero).  In iteration t: K of
+    // t + 2 and V of t + 1 come in; the one barrier stands between the last
+    // reads of the buffers that they go to and the stores.
+    uint32_t row = row_of(t0, page_of(t0)), row1 = row_of(t0 + 1, page_of(t0 + 1));
+    unsigned long long have = __ballot(row != kNoRow), have1 = __ballot(row1 != kNoRow);
+    Stage st, sv;
+    {
+      Stage s1, s2;
+      load_tile(st, c.k, c.k_scale, row);
+      load_tile(s1, c.v, c.v_scale, row);
+      load_tile(s2, c.k, c.k_scale, row1);
+      put(st, k_tile(t0), std::false_type{});
+      store_v(s1, t0, have);
+      put(s2, k_tile(t0 + 1), std::false_type{});
+    }
+    int page = page_of(t0 + 2);
+    for (int i = tid; i < 32 * C::chunks; i += C::threads)
+      *(uint4 *)(v_tile(t0 + 1) + 32 * C::row_bytes + 16 * i) = make_uint4(0, 0, 0, 0);
+    if (lane == 0) flags[NW + wave] = 0;            // nothing to add of it
     __syncthreads();
+    f32x16 sa, sb;
+    Weights wa, wb;
+#pragma unroll
+    for (int i = 0; i < (F == FMT_F32 ? 16 : 8); ++i) wb[i] = 0;
+    if (has_rows) {
+      const uint32_t ka = k_from(t0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sa[i] = 0.0f;
+      static_for<QP>([&](auto n) MOE_INLINE { mul_k(sa, read_k(ka, n, 0), n); });
+    }
     for (int t = t0; t < t1; ++t) {
-      const int stage = (t - t0) & 1, k0 = range.key(t);
-      const unsigned long long there_now = there;
-      row = row_of(t + 1, page);
-      there = __ballot(row != kNoRow);
-      load_tile(c.k, c.k_scale, row);
+      const uint32_t row2 = row_of(t + 2, page);
+      load_tile(st, c.k, c.k_scale, row2);
+      load_tile(sv, c.v, c.v_scale, row1);
+      page = page_of(t + 3);
       __builtin_amdgcn_sched_barrier(0);
-      const bool seen = has_rows && k0 < any_hi && (k0 + BK > any_lo || k0 < a.sinks);
-      const bool inner = k0 + BK <= all_hi && (k0 >= all_lo || k0 + BK <= a.sinks) && there_now == ~0ull;
-      f32x16 sc[KT][QT];
-      if (seen) scores(stage, sc);
-      __builtin_amdgcn_sched_barrier(0);
-      store_k(stage ^ 1);
-      load_tile(c.v, c.v_scale, row);
-      page = page_of(t + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      if (seen) {
-        if (!inner) {
-          static_for<KT>([&](auto kt) MOE_INLINE {
-            uint32_t bits = (uint32_t)(there_now >> (32 * kt)) >> (4 * hf);
-            asm volatile("" : "+v"(bits));                 // keeps the masks out of inner tiles
-            const int base = k0 + 32 * kt + 4 * hf;
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-              const int below = hi[qt] - base, from = lo[qt] - base, sink = a.sinks - base;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int j = 8 * (i / 4) + i % 4;
-                const bool see = ((bits >> j) & 1) && j < below && (j >= from || j < sink);
-                sc[kt][qt][i] = see ? sc[kt][qt][i] : -INFINITY;
-              }
-            }
-          });
-        }
-        i32x4 pw[KT][QT][2];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kt][qt][i]);
-          top = max_half(top) * a.scale;                   // the scale is positive
-          if (__ballot(top > mx[qt] + 8.0f)) {
-            const float now = top > mx[qt] + 8.0f ? top : mx[qt];
-            const float alpha = __builtin_amdgcn_exp2f(mx[qt] - now);
-            mx[qt] = now;
-            sum[qt] *= alpha;
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[qt][d][i] *= alpha;
-          }
-          float part = 0.0f;
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float p = __builtin_amdgcn_exp2f(fmaf(sc[kt][qt][i], a.scale, -mx[qt]));
-              sc[kt][qt][i] = p;
-              part += p;
-            }
-            if constexpr (F != FMT_F32)
-#pragma unroll
-              for (int st = 0; st < 2; ++st)
-                pw[kt][qt][st] = i32x4{(int)bf16_pack2(sc[kt][qt][8 * st], sc[kt][qt][8 * st + 1]),
-                                       (int)bf16_pack2(sc[kt][qt][8 * st + 2], sc[kt][qt][8 * st + 3]),
-                                       (int)bf16_pack2(sc[kt][qt][8 * st + 4], sc[kt][qt][8 * st + 5]),
-                                       (int)bf16_pack2(sc[kt][qt][8 * st + 6], sc[kt][qt][8 * st + 7])};
-          }
-          sum[qt] += part;
-        }
-        uint32_t addr = v_addr + (2 * stage + 1) * C::tile;
-        asm volatile("" : "+v"(addr));
-        static_for<KT>([&](auto kt) MOE_INLINE {
-          static_for<DT>([&](auto dt) MOE_INLINE { add_pv(addr, kt, dt, sc[kt], pw[kt]); });
-        });
-        if (partial(t) && (flags[4 * stage] | flags[4 * stage + 1] | flags[4 * stage + 2] | flags[4 * stage + 3]))
-          add_not_finite(k0);
-      }
-      if (t + 1 < t1) store_v(t + 1, stage ^ 1, there);
+      if (has_rows) step(std::integral_constant<int, 0>{}, t, have, sa, sb, wa, wb);
       __syncthreads();
+      put(st, k_tile(t + 2), std::false_type{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (has_rows) step(std::integral_constant<int, 1>{}, t, have, sb, sa, wb, wa);
+      have = have1;
+      have1 = __ballot(row2 != kNoRow);
+      row1 = row2;
+      if (t + 1 < t1) store_v(sv, t + 1, have);
+    }
+    if (has_rows) {
+      const uint32_t va = v_from(t1 - 1);
+      static_for<PV * DT>([&](auto n) MOE_INLINE { mul_v(wb, read_v(va, n, 1), n); });
+      add_not_finite(t1 - 1, 1);
     }
   }
 
   // ---- results
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    const int m = m0 + 32 * qt + q32;
-    const float l = sum_half(sum[qt]);
-    if (m >= nrows) continue;
+  const float l = sum_half(sum);
+  if (in) {
     if (splits == 1) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int tok = m / a.group, hq = h * a.group + m % a.group;
-      const long long at = ((long long)(g.r0 + tok) * a.heads + hq) * HD + 4 * hf;
+      const long long at = ((long long)(g.r0 + own_tok) * a.heads + hq) * HD + 4 * hf;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const float v0 = o[qt][d][4 * b] * inv, v1 = o[qt][d][4 * b + 1] * inv;
-          const float v2 = o[qt][d][4 * b + 2] * inv, v3 = o[qt][d][4 * b + 3] * inv;
+          const float v0 = o[d][4 * b] * inv, v1 = o[d][4 * b + 1] * inv;
+          const float v2 = o[d][4 * b + 2] * inv, v3 = o[d][4 * b + 3] * inv;
           if constexpr (F == FMT_F32)
             *(f32x4 *)((float *)a.out + at + 32 * d + 8 * b) = f32x4{v0, v1, v2, v3};
           else
             *(uint2 *)((uint16_t *)a.out + at + 32 * d + 8 * b) = make_uint2(bf16_pack2(v0, v1), bf16_pack2(v2, v3));
         }
     } else {
-      float *part = a.part + ((long long)u * c.kv_heads + h) * splits * ROWS * (HD + 2) +
-                    (long long)split * ROWS * (HD + 2);
+      float *part = a.part + (((long long)u * c.kv_heads + h) * splits + split) * ROWS * (HD + 2);
       const int r = m - rt0;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
           *(f32x4 *)(part + r * HD + 32 * d + 8 * b + 4 * hf) =
-              f32x4{o[qt][d][4 * b], o[qt][d][4 * b + 1], o[qt][d][4 * b + 2], o[qt][d][4 * b + 3]};
+              f32x4{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
       if (hf == 0) {
-        part[ROWS * HD + 2 * r] = mx[qt];
+        part[ROWS * HD + 2 * r] = mx;
         part[ROWS * HD + 2 * r + 1] = l;
       }
     }
@@ -451,9 +494,9 @@ __global__ __launch_bounds__(256, OCC) void attn_tile_kernel(AttnArgs a, int spl
 }
 
 // Join the splits of a unit: HD / 4 threads a row, 4 columns each.
-template <int F, int HD, int BK, int QT>
+template <int F, int HD, int NW>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int splits) {
-  constexpr int ROWS = TileCfg<F, HD, BK, QT>::rows, COLS = HD / 4, PER = 256 / COLS;
+  constexpr int ROWS = TileCfg<F, HD, NW>::rows, COLS = HD / 4, PER = 256 / COLS;
   const KvArgs &c = a.c;
   const int groups = ROWS / PER;                    // workgroups a unit
   const int gr = blockIdx.x % groups, h = blockIdx.x / groups % c.kv_heads, u = blockIdx.x / groups / c.kv_heads;
@@ -483,9 +526,9 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(AttnArgs a, int spl
 }
 
 namespace {
-template <int F, int HD, int BK, int QT, int OCC>
+template <int F, int HD, int NW, int OCC>
 struct TileLaunch {
-  using C = TileCfg<F, HD, BK, QT>;
+  using C = TileCfg<F, HD, NW>;
   // row tiles of all sequences, at most
   static long long units(const AttnArgs &a) {
     const long long each = ((long long)a.c.max_rows * a.group + C::rows - 1) / C::rows * a.c.seqs;
@@ -495,13 +538,13 @@ struct TileLaunch {
   // Enough workgroups for every CU (OCC each), but four key tiles at least in
   // a run where the longest possible row sees that many.
   static int splits(const AttnArgs &a) {
-    const long long wgs = units(a) * a.c.kv_heads, want = 256 * OCC;
+    const long long wgs = units(a) * a.c.kv_heads, want = 256 * OCC * 4 / NW;
     long long keys = (long long)a.c.max_pages << a.c.page_shift;
     if (a.window) {
       const long long seen = (long long)a.window + a.sinks + C::rows / a.group + 1;
       keys = keys < seen ? keys : seen;
     }
-    const long long most = keys / (4 * BK) < 1 ? 1 : keys / (4 * BK);
+    const long long most = keys / (4 * C::BK) < 1 ? 1 : keys / (4 * C::BK);
     const long long s = want / wgs;
     return (int)(s < 1 ? 1 : s < most ? s : most);
   }
@@ -516,31 +559,27 @@ struct TileLaunch {
   static hipError_t run(const AttnArgs &a, hipStream_t st) {
     const int s = splits(a);
     const long long u = units(a) * a.c.kv_heads, grid = u * s;
-    static const hipError_t once = hipFuncSetAttribute((const void *)attn_tile_kernel<F, HD, BK, QT, OCC>,
+    static const hipError_t once = hipFuncSetAttribute((const void *)attn_tile_kernel<F, HD, NW, OCC>,
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
     if (once != hipSuccess) return once;
-    attn_tile_kernel<F, HD, BK, QT, OCC><<<(unsigned)grid, 256, C::lds, st>>>(a, s);
+    attn_tile_kernel<F, HD, NW, OCC><<<(unsigned)grid, C::threads, C::lds, st>>>(a, s);
     if (s > 1)
-      attn_tile_join_kernel<F, HD, BK, QT><<<(unsigned)(u * (C::rows / (1024 / HD))), 256, 0, st>>>(a, s);
+      attn_tile_join_kernel<F, HD, NW><<<(unsigned)(u * (C::rows / (1024 / HD))), 256, 0, st>>>(a, s);
     return hipGetLastError();
   }
 };
 
 template <typename Fn>
 auto pick_tile(const KvArgs &c, Fn &&f) {
-  if (c.fmt == FMT_F32) {
-    if (c.head_dim == 64) return f(TileLaunch<FMT_F32, 64, 64, 1, 2>{});
-    if (c.head_dim == 128) return f(TileLaunch<FMT_F32, 128, 32, 1, 1>{});
-    return f(TileLaunch<FMT_F32, 256, 32, 1, 1>{});
-  }
+  if (c.fmt == FMT_F32) return c.head_dim == 64 ? f(TileLaunch<FMT_F32, 64, 4, 2>{}) : f(TileLaunch<FMT_F32, 128, 4, 1>{});
   if (c.fmt == FMT_BF16) {
-    if (c.head_dim == 64) return f(TileLaunch<FMT_BF16, 64, 64, 1, 2>{});
-    if (c.head_dim == 128) return f(TileLaunch<FMT_BF16, 128, 64, 1, 2>{});
-    return f(TileLaunch<FMT_BF16, 256, 32, 1, 1>{});
+    if (c.head_dim == 64) return f(TileLaunch<FMT_BF16, 64, 4, 2>{});
+    if (c.head_dim == 128) return f(TileLaunch<FMT_BF16, 128, 8, 2>{});
+    return f(TileLaunch<FMT_BF16, 256, 4, 1>{});
   }
-  if (c.head_dim == 64) return f(TileLaunch<FMT_MX8, 64, 64, 1, 2>{});
-  if (c.head_dim == 128) return f(TileLaunch<FMT_MX8, 128, 64, 1, 2>{});
-  return f(TileLaunch<FMT_MX8, 256, 32, 1, 1>{});
+  if (c.head_dim == 64) return f(TileLaunch<FMT_MX8, 64, 4, 2>{});
+  if (c.head_dim == 128) return f(TileLaunch<FMT_MX8, 128, 8, 2>{});
+  return f(TileLaunch<FMT_MX8, 256, 4, 1>{});
 }
 }  // namespace
 

@@ -85,8 +85,12 @@ moe_status attn_args(const moe_kv_cache *cache, const moe_kv_batch *batch, int h
 }
 
 // Which kernel: up to 32 rows (tokens x heads of a group) a sequence fit the
-// row kernel's tile, which reads the keys once and is bound by that.
-bool few_rows(const AttnArgs &a) { return (long long)a.c.max_rows * a.group <= 32; }
+// row kernel's tile, which reads the keys once and is bound by that.  fp32
+// with head_dim 256 always goes there: two tiles of keys and values would not
+// fit the LDS.
+bool few_rows(const AttnArgs &a) {
+  return (long long)a.c.max_rows * a.group <= 32 || (a.c.fmt == FMT_F32 && a.c.head_dim == 256);
+}
 
 size_t workspace(const AttnArgs &a) {
   if (a.c.rows <= 0) return 0;
