@@ -40,6 +40,7 @@ struct TileCfg {
   // what others do)
   static constexpr int parts = HD / 16 < NW ? HD / 16 : NW, codes = HD / parts, scales = codes > 32 ? codes / 32 : 1;
   static constexpr int pieces = F == FMT_MX8 ? codes / 16 : tile / 16 / threads;
+  static constexpr int span = F == FMT_MX8 ? 1 : 64 / chunks;   // keys of a wave's piece (of one page)
   static constexpr int QP = row_bytes / 32;                // 16-byte query pieces a lane
   static constexpr int DT = HD / 32;
   // chunk c of key row r is stored at chunk c ^ swz(r)
@@ -95,7 +96,8 @@ template <int F, int HD, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int splits) {
   using C = TileCfg<F, HD, NW>;
   constexpr int ROWS = C::rows, BK = C::BK, DT = C::DT, QP = C::QP, NP = C::pieces;
-  extern __shared__ __align__(16) uint8_t lds[];           // K0 V0 K1 V1, flags
+  constexpr int KEYS = F == FMT_MX8 ? 1 : NP;              // places that a thread stages pieces from
+  extern __shared__ __align__(16) uint8_t lds[];           // K0 K1 V0 V1, flags
   int *flags = (int *)(lds + 4 * C::tile);                 // [stage][wave]
   const int tid = threadIdx.x, lane = tid & 63, q32 = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -126,9 +128,8 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     for (int p = 0; p < QP; ++p) q[p] = in ? *(const i32x4 *)(qp + 32 * p) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
   }
   const RowMask mask(g, own_tok, in, a.window, a.sinks);
-  // the wave's tokens, and the keys that all of them see
-  const int wtok_a = m0 / a.group, wtok_b = (min(m0 + 32, nrows) - 1) / a.group;
-  const int all_hi = min(g.pos0 + wtok_a + 1, g.len), all_lo = a.window ? g.pos0 + wtok_b - a.window + 1 : 0;
+  // keys that all rows of the workgroup see (but for the sinks)
+  const int all_hi = min(g.pos0 + tok_a + 1, g.len), all_lo = a.window ? g.pos0 + tok_b - a.window + 1 : 0;
 
   f32x16 o[DT];
   float mx = kNegBig, sum = 0.0f;
@@ -139,30 +140,54 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
 
   // ---- staging
   const int32_t *pages = c.table + (long long)s * c.max_pages;
-  // The table's entry for key `lane` of tile t, and the key's row in the pool.
-  // As in the row kernel no load of the loop stands under a condition: past the
-  // last tile, and for keys without a page, row 0 is read.
-  auto page_of = [&](int t) MOE_INLINE {
-    return pages[min((range.key(min(t, t1 - 1)) + lane) >> c.page_shift, c.max_pages - 1)];
+  // key of the tile that piece p of this thread belongs to (MX: all pieces)
+  auto piece_key = [&](int p) MOE_INLINE {
+    if constexpr (F == FMT_MX8) return tid / C::parts % BK;
+    else return (p * C::threads + tid) / C::chunks;
   };
-  auto row_of = [&](int t, int page) MOE_INLINE {
-    const int key = range.key(t) + lane;
-    return t < t1 && key < g.len ? pool_row(c, page, h, key) : kNoRow;
+  // The table's entry for key `lane` of tile t (MX: and for the thread's piece),
+  // and the rows of the pool there.  A bf16 or fp32 piece of a wave is `span`
+  // consecutive keys, all in one page (pages hold 8 keys or more), so its row is
+  // a scalar, taken from the lane that looked it up, and its lanes read a
+  // contiguous KiB.  As in the row kernel no load of the loop stands under a
+  // condition: past the last tile, and for keys without a page, row 0 is read.
+  struct Pages {
+    int lane, piece;
+  };
+  auto pages_of = [&](int t) MOE_INLINE {
+    const int k0 = range.key(min(t, t1 - 1));
+    Pages r;
+    r.lane = pages[min((k0 + lane) >> c.page_shift, c.max_pages - 1)];
+    r.piece = F == FMT_MX8 ? pages[min((k0 + piece_key(0)) >> c.page_shift, c.max_pages - 1)] : 0;
+    return r;
+  };
+  struct Rows {
+    uint32_t piece[KEYS];
+    unsigned long long have;                               // bit j: key j of the tile exists
+  };
+  auto rows_of = [&](int t, const Pages &page) MOE_INLINE {
+    const int k0 = range.key(t), left = t < t1 ? g.len - k0 : 0;
+    const bool in = (unsigned)page.lane < (unsigned)c.num_pages && lane < left;
+    Rows r;
+    r.have = __ballot(in);
+    if constexpr (F == FMT_MX8) {
+      const uint32_t row = pool_row(c, page.piece, h, k0 + piece_key(0));
+      r.piece[0] = row != kNoRow && piece_key(0) < left ? row : 0u;
+    } else {
+      const uint32_t row = in ? pool_row(c, page.lane, h, k0 + lane) : 0u;
+#pragma unroll
+      for (int p = 0; p < KEYS; ++p) r.piece[p] = __builtin_amdgcn_readlane(row, (p * NW + wave) * C::span);
+    }
+    return r;
   };
   // a tile's K or V on its way
   struct Stage {
     i32x4 d[NP];
     uint32_t scale[C::scales];
   };
-  // key of the tile that piece p of this thread belongs to
-  auto piece_key = [&](int p) MOE_INLINE {
-    if constexpr (F == FMT_MX8) return tid / C::parts % BK;
-    else return (p * C::threads + tid) / C::chunks;
-  };
-  auto load_tile = [&](Stage &st, const uint8_t *pool, const uint8_t *scale, uint32_t row) MOE_INLINE {
-    const uint32_t safe = row == kNoRow ? 0u : row;
+  auto load_tile = [&](Stage &st, const uint8_t *pool, const uint8_t *scale, const Rows &r) MOE_INLINE {
     if constexpr (F == FMT_MX8) {
-      const long long at = (long long)__shfl(safe, piece_key(0), 64) * HD + tid % C::parts * C::codes;
+      const long long at = (long long)r.piece[0] * HD + tid % C::parts * C::codes;
 #pragma unroll
       for (int p = 0; p < NP; ++p) st.d[p] = *(const i32x4 *)(pool + at + 16 * p);
 #pragma unroll
@@ -170,8 +195,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     } else {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        st.d[p] = *(const i32x4 *)(pool + (long long)__shfl(safe, piece_key(p), 64) * C::row_bytes +
-                                   (p * C::threads + tid) % C::chunks * 16);
+        st.d[p] = *(const i32x4 *)(pool + (unsigned long long)r.piece[p] * C::row_bytes + 16u * lane);
     }
   };
   // (`finite`: zeros in place of what is not)
@@ -195,13 +219,14 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       for (int p = 0; p < NP; ++p) chunk(piece_key(p), (p * C::threads + tid) % C::chunks, __builtin_bit_cast(uint4, st.d[p]));
     }
   };
-  // Tiles in which some of the workgroup's rows see a key that others do not.
-  auto partial = [&](int t) MOE_INLINE {
+  // Tiles whose keys all exist and are seen by all rows: no masks, and no need
+  // to look for values that are not finite.
+  auto plain = [&](int t, unsigned long long have) MOE_INLINE {
     const int k0 = range.key(t);
-    return tok_b > tok_a && (k0 + BK > g.pos0 + tok_a + 1 || (a.window && k0 <= g.pos0 + tok_b - a.window));
+    return k0 + BK <= all_hi && k0 >= all_lo && have == ~0ull;
   };
-  auto k_tile = [&](int t) MOE_INLINE { return lds + 2 * ((t - t0) & 1) * C::tile; };
-  auto v_tile = [&](int t) MOE_INLINE { return lds + (2 * ((t - t0) & 1) + 1) * C::tile; };
+  auto k_tile = [&](int t) MOE_INLINE { return lds + ((t - t0) & 1) * C::tile; };
+  auto v_tile = [&](int t) MOE_INLINE { return lds + (2 + ((t - t0) & 1)) * C::tile; };
   auto store_v = [&](Stage &st, int t, unsigned long long have) MOE_INLINE {
     if (have != ~0ull) {                                   // V of keys that do not exist: zeros
 #pragma unroll
@@ -212,7 +237,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
           for (int i = 0; i < C::scales; ++i) st.scale[i] = 0;
         }
     }
-    if (partial(t)) {
+    if (!plain(t, have)) {
       put(st, v_tile(t), std::true_type{});
       bool bad = false;
       if constexpr (F == FMT_MX8)
@@ -230,14 +255,34 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
   };
 
   // ---- products, of halves of a tile (32 keys).  Addresses within LDS: the
-  // swizzle makes all of a lane's reads XORs and offsets of its first; they are
-  // made anew from an opaque copy, which is cheaper than registers for them.
-  // K: lane q32 reads key row q32 of a half, chunk 2 p + hf
-  const uint32_t k_addr = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
-  const uint32_t v_addr =
-      F == FMT_F32 ? 4 * hf * C::row_bytes + (((q32 >> 2) ^ C::swz(4 * hf)) << 4) + 4 * (q32 & 3)
-                   : (4 * hf + ((lane & 15) >> 2)) * C::row_bytes + 8 * (lane & 1) +
-                         (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(4 * hf + ((lane & 15) >> 2))) << 4);
+  // swizzle makes a lane's reads XORs and offsets of its first.  K: lane q32
+  // reads key row q32 of a half, chunk 2 p + hf.
+  // The buffers of the next tile are an XOR away, too (tile is a power of two).
+  static_assert((C::tile & (C::tile - 1)) == 0, "buffers differ in one bit");
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t *)lds;
+  uint32_t k_addr[QP], v_addr[F == FMT_F32 ? 4 * DT : 2 * DT];
+  {
+    const uint32_t k0 = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
+    const uint32_t v0 =
+        F == FMT_F32 ? 4 * hf * C::row_bytes + (((q32 >> 2) ^ C::swz(4 * hf)) << 4) + 4 * (q32 & 3)
+                     : (4 * hf + ((lane & 15) >> 2)) * C::row_bytes + 8 * (lane & 1) +
+                           (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(4 * hf + ((lane & 15) >> 2))) << 4);
+#pragma unroll
+    for (int p = 0; p < QP; ++p) k_addr[p] = lds0 + (k0 ^ (32 * p));
+    // the first V buffer that is read is that of the tile before the first
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int x = 0; x < (F == FMT_F32 ? 4 : 2); ++x)
+        v_addr[(F == FMT_F32 ? 4 : 2) * d + x] =
+            lds0 + 3 * C::tile + (F == FMT_F32 ? v0 ^ (128 * d) ^ (16 * x) : v0 ^ (64 * d) ^ (32 * x));
+  }
+  auto other_buffers = [&]() MOE_INLINE {
+#pragma unroll
+    for (auto &x : k_addr) x ^= C::tile;
+#pragma unroll
+    for (auto &x : v_addr) x ^= C::tile;
+  };
   // The products of a step, in slots: even ones a piece of the scores' head_dim
   // (S^T; element i is key 8 (i / 4) + 4 hf + i % 4 of the half), odd ones 16
   // keys (fp32: 4) of the values for 32 columns.  So neighbours do not wait for
@@ -246,23 +291,25 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
   static_assert(QP == PV * DT, "as many pieces of scores as of values");
   // the softmax weights of a half: fp32, or bf16 in pairs
   using Weights = std::conditional_t<F == FMT_F32, f32x16, i32x8>;
-  auto read_k = [&](uint32_t addr, auto n, int half) MOE_INLINE {
-    return *(const i32x4 *)(lds + (addr ^ (32 * n)) + 32 * half * C::row_bytes);
+  auto read_k = [&](auto n, int half) MOE_INLINE {
+    using P = const __attribute__((address_space(3))) i32x4 *;
+    return *(P)(size_t)(k_addr[n] + 32 * half * C::row_bytes);
   };
-  auto read_v = [&](uint32_t addr, auto n, int half) MOE_INLINE {
+  auto read_v = [&](auto n, int half) MOE_INLINE {
     constexpr int dt = n % DT, part = n / DT;
     i32x4 f;
     if constexpr (F == FMT_F32) {
+      using P = const __attribute__((address_space(3))) int *;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        f[i] = *(const int *)(lds + (addr ^ (16 * i) ^ (128 * dt)) + (32 * half + 8 * part + i) * C::row_bytes);
+        f[i] = *(P)(size_t)(v_addr[4 * dt + i] + (32 * half + 8 * part + i) * C::row_bytes);
     } else {
-      using lds_i32x2 = __attribute__((address_space(3))) s16x4;
       // a group of 16 lanes reads 4 keys x 16 columns, transposed
-      const i32x2 v0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i32x2 *)(
-          lds + (addr ^ (64 * dt)) + (32 * half + 16 * part) * C::row_bytes)));
-      const i32x2 v1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i32x2 *)(
-          lds + (addr ^ (64 * dt) ^ 32) + (32 * half + 16 * part + 8) * C::row_bytes)));
+      using P = __attribute__((address_space(3))) s16x4 *;
+      const i32x2 v0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (P)(size_t)(v_addr[2 * dt] + (32 * half + 16 * part) * C::row_bytes)));
+      const i32x2 v1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (P)(size_t)(v_addr[2 * dt + 1] + (32 * half + 16 * part + 8) * C::row_bytes)));
       f = __builtin_shufflevector(v0, v1, 0, 1, 2, 3);
     }
     return f;
@@ -289,20 +336,10 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
                                                      o[dt], 0, 0, 0);
     }
   };
-  auto k_from = [&](int t) MOE_INLINE {
-    uint32_t addr = k_addr + (uint32_t)(k_tile(t) - lds);
-    asm volatile("" : "+v"(addr));
-    return addr;
-  };
-  auto v_from = [&](int t) MOE_INLINE {
-    uint32_t addr = v_addr + (uint32_t)(v_tile(t) - lds);
-    asm volatile("" : "+v"(addr));
-    return addr;
-  };
-  // what is not finite of V in half `half` of a partial tile (zeros in LDS)
+  // what is not finite of V in half `half` of a tile that is not plain (zeros
+  // in LDS)
   auto add_not_finite = [&](int t, int half) MOE_INLINE {
     const int *f = flags + NW * ((t - t0) & 1);
-    if (!partial(t)) return;
     int any = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) any |= f[i];
@@ -330,14 +367,23 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
   // under the softmax of the same wave.
   //   half 0: next = half 1 of tile t, last = half 1 of tile t - 1
   //   half 1: next = half 0 of tile t + 1, last = half 0 of tile t
-  auto step = [&](auto half, int t, unsigned long long have, f32x16 &cur, f32x16 &next, Weights &w,
-                  const Weights &last) MOE_INLINE {
-    const int k0 = range.key(t) + 32 * half;
-    const uint32_t have32 = (uint32_t)(have >> (32 * half));
-    const bool inner = k0 + 32 <= all_hi && (k0 >= all_lo || k0 + 32 <= a.sinks) && have32 == ~0u;
-    if (!inner) {
-      uint32_t bits = have32 >> (4 * hf);
-      asm volatile("" : "+v"(bits));               // keeps the masks out of inner halves
+  // begin issues the first reads; what stands between it and step runs under them.
+  constexpr int AHEAD = 2;                         // slots between a read and its product
+  i32x4 frag[AHEAD];
+  auto read = [&](auto half, auto n) MOE_INLINE {
+    if constexpr (n % 2) frag[n % AHEAD] = read_v(std::integral_constant<int, n / 2>{}, 1 - half);
+    else frag[n % AHEAD] = read_k(std::integral_constant<int, n / 2>{}, 1 - half);
+  };
+  auto begin = [&](auto half) MOE_INLINE {
+    static_for<AHEAD>([&](auto n) MOE_INLINE { read(half, n); });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step = [&](auto half, int t, unsigned long long have, bool is_plain, bool v_plain, f32x16 &cur, f32x16 &next,
+                  Weights &w, const Weights &last) MOE_INLINE {
+    if (!is_plain) {
+      const int k0 = range.key(t) + 32 * half;
+      uint32_t bits = (uint32_t)(have >> (32 * half)) >> (4 * hf);
+      asm volatile("" : "+v"(bits));               // keeps the masks out of plain tiles
       const int base = k0 + 4 * hf, below = mask.hi - base, from = mask.lo - base, sink = a.sinks - base;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -346,17 +392,9 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
         cur[i] = see ? cur[i] : -INFINITY;
       }
     }
-    // Slots in this order, the reads AHEAD slots before their product.  The
-    // maximum comes first, the exponentials are spread over the slots, and
-    // their sum and rounding follow one slot behind.
-    constexpr int AHEAD = 4, FIRST = 2, SPAN = SLOTS - FIRST - 1;
-    const uint32_t ka = k_from(half ? t + 1 : t), va = v_from(half ? t : t - 1);
-    i32x4 frag[AHEAD];
-    auto read = [&](auto n) MOE_INLINE {
-      if constexpr (n % 2) frag[n % AHEAD] = read_v(va, std::integral_constant<int, n / 2>{}, 1 - half);
-      else frag[n % AHEAD] = read_k(ka, std::integral_constant<int, n / 2>{}, 1 - half);
-    };
-    static_for<AHEAD>([&](auto n) MOE_INLINE { read(n); });
+    // The slots in this order.  The maximum comes first, the exponentials are
+    // spread over the slots, and their sum and rounding follow one slot behind.
+    constexpr int FIRST = 2, SPAN = SLOTS - FIRST - 1;
     __builtin_amdgcn_sched_barrier(0);
     float top = -INFINITY, now = 0.0f, alpha = 0.0f, part[2] = {0.0f, 0.0f};
     static_for<SLOTS>([&](auto n) MOE_INLINE {
@@ -365,7 +403,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
         for (int i = 0; i < 16; ++i) next[i] = 0.0f;
       if constexpr (n % 2) mul_v(last, frag[n % AHEAD], std::integral_constant<int, n / 2>{});
       else mul_k(next, frag[n % AHEAD], std::integral_constant<int, n / 2>{});
-      if constexpr (n + AHEAD < SLOTS) read(std::integral_constant<int, n + AHEAD>{});
+      if constexpr (n + AHEAD < SLOTS) read(half, std::integral_constant<int, n + AHEAD>{});
       if constexpr (n == 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, cur[i]);
@@ -392,7 +430,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     if constexpr (F == FMT_F32) w = cur;
     sum = fmaf(sum, alpha, part[0] + part[1]);
     asm volatile("" : "+v"(w), "+v"(sum));         // ahead of the branches below
-    add_not_finite(half ? t : t - 1, 1 - half);
+    if (!v_plain) add_not_finite(half ? t : t - 1, 1 - half);
     const bool moved = now > mx;
     mx = now;
     if (__ballot(moved)) {
@@ -408,53 +446,59 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     // half before the first (whose weights are zero).  In iteration t: K of
     // t + 2 and V of t + 1 come in; the one barrier stands between the last
     // reads of the buffers that they go to and the stores.
-    uint32_t row = row_of(t0, page_of(t0)), row1 = row_of(t0 + 1, page_of(t0 + 1));
-    unsigned long long have = __ballot(row != kNoRow), have1 = __ballot(row1 != kNoRow);
-    Stage st, sv;
+    constexpr std::integral_constant<int, 0> first{};
+    constexpr std::integral_constant<int, 1> second{};
+    Rows row = rows_of(t0, pages_of(t0)), row1 = rows_of(t0 + 1, pages_of(t0 + 1));
+    Stage sk, sv;
     {
-      Stage s1, s2;
-      load_tile(st, c.k, c.k_scale, row);
-      load_tile(s1, c.v, c.v_scale, row);
-      load_tile(s2, c.k, c.k_scale, row1);
-      put(st, k_tile(t0), std::false_type{});
-      store_v(s1, t0, have);
-      put(s2, k_tile(t0 + 1), std::false_type{});
+      Stage s0;
+      load_tile(s0, c.k, c.k_scale, row);
+      load_tile(sv, c.v, c.v_scale, row);
+      load_tile(sk, c.k, c.k_scale, row1);
+      put(s0, k_tile(t0), std::false_type{});
+      store_v(sv, t0, row.have);
+      put(sk, k_tile(t0 + 1), std::false_type{});
     }
-    int page = page_of(t0 + 2);
+    Pages page = pages_of(t0 + 2);
     for (int i = tid; i < 32 * C::chunks; i += C::threads)
       *(uint4 *)(v_tile(t0 + 1) + 32 * C::row_bytes + 16 * i) = make_uint4(0, 0, 0, 0);
-    if (lane == 0) flags[NW + wave] = 0;            // nothing to add of it
     __syncthreads();
     f32x16 sa, sb;
     Weights wa, wb;
 #pragma unroll
     for (int i = 0; i < (F == FMT_F32 ? 16 : 8); ++i) wb[i] = 0;
     if (has_rows) {
-      const uint32_t ka = k_from(t0);
 #pragma unroll
       for (int i = 0; i < 16; ++i) sa[i] = 0.0f;
-      static_for<QP>([&](auto n) MOE_INLINE { mul_k(sa, read_k(ka, n, 0), n); });
+      static_for<QP>([&](auto n) MOE_INLINE { mul_k(sa, read_k(n, 0), n); });
     }
+    bool is_plain = plain(t0, row.have), last_plain = true;
     for (int t = t0; t < t1; ++t) {
-      const uint32_t row2 = row_of(t + 2, page);
-      load_tile(st, c.k, c.k_scale, row2);
+      if (has_rows) begin(first);
+      const Rows row2 = rows_of(t + 2, page);
+      load_tile(sk, c.k, c.k_scale, row2);
       load_tile(sv, c.v, c.v_scale, row1);
-      page = page_of(t + 3);
-      __builtin_amdgcn_sched_barrier(0);
-      if (has_rows) step(std::integral_constant<int, 0>{}, t, have, sa, sb, wa, wb);
-      __syncthreads();
-      put(st, k_tile(t + 2), std::false_type{});
-      __builtin_amdgcn_sched_barrier(0);
-      if (has_rows) step(std::integral_constant<int, 1>{}, t, have, sb, sa, wb, wa);
-      have = have1;
-      have1 = __ballot(row2 != kNoRow);
+      page = pages_of(t + 3);
+      if (has_rows) step(first, t, row.have, is_plain, last_plain, sa, sb, wa, wb);
+      other_buffers();
+      // The barrier, without waiting for the loads: LDS accesses are done.
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (has_rows) {
+        begin(second);
+        step(second, t, row.have, is_plain, is_plain, sb, sa, wb, wa);
+      }
+      row = row1;
       row1 = row2;
-      if (t + 1 < t1) store_v(sv, t + 1, have);
+      put(sk, k_tile(t + 2), std::false_type{});
+      last_plain = is_plain;
+      if (t + 1 < t1) {
+        is_plain = plain(t + 1, row.have);
+        store_v(sv, t + 1, row.have);
+      }
     }
     if (has_rows) {
-      const uint32_t va = v_from(t1 - 1);
-      static_for<PV * DT>([&](auto n) MOE_INLINE { mul_v(wb, read_v(va, n, 1), n); });
-      add_not_finite(t1 - 1, 1);
+      static_for<PV * DT>([&](auto n) MOE_INLINE { mul_v(wb, read_v(n, 1), n); });
+      if (!last_plain) add_not_finite(t1 - 1, 1);
     }
   }
 

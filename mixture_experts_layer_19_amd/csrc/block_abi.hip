@@ -85,11 +85,11 @@ moe_status attn_args(const moe_kv_cache *cache, const moe_kv_batch *batch, int h
 }
 
 // Which kernel: up to 32 rows (tokens x heads of a group) a sequence fit the
-// row kernel's tile, which reads the keys once and is bound by that.  fp32
-// with head_dim 256 always goes there: two tiles of keys and values would not
-// fit the LDS.
+// row kernel's tile, which reads the keys once and is bound by that.  So go
+// fp32 with head_dim 256, whose two tiles of keys and values would not fit the
+// LDS, and pages of fewer than 8 keys, which a wave's load would straddle.
 bool few_rows(const AttnArgs &a) {
-  return (long long)a.c.max_rows * a.group <= 32 || (a.c.fmt == FMT_F32 && a.c.head_dim == 256);
+  return (long long)a.c.max_rows * a.group <= 32 || (a.c.fmt == FMT_F32 && a.c.head_dim == 256) || a.c.page_shift < 3;
 }
 
 size_t workspace(const AttnArgs &a) {
