@@ -579,10 +579,13 @@ struct TileLaunch {
     const long long all = (long long)a.c.rows * a.group / C::rows + a.c.seqs;
     return each < all ? each : all;
   }
-  // Enough workgroups for every CU (OCC each), but four key tiles at least in
-  // a run where the longest possible row sees that many.
+  // Enough workgroups for every CU (two of four waves where they fit), but four
+  // key tiles at least in a run where the longest possible row sees that many.
+  // fp32 of head_dim 64 is bound by its slow matrix instructions and by uneven
+  // units: twice as many (12 sequences of 1-211 tokens over up to 900 keys, 16
+  // heads: 110 -> 87 us; four times: 103; bf16 and larger heads lose).
   static int splits(const AttnArgs &a) {
-    const long long wgs = units(a) * a.c.kv_heads, want = 256 * OCC * 4 / NW;
+    const long long wgs = units(a) * a.c.kv_heads, want = 256 * OCC * 4 / NW * (F == FMT_F32 && HD == 64 ? 2 : 1);
     long long keys = (long long)a.c.max_pages << a.c.page_shift;
     if (a.window) {
       const long long seen = (long long)a.window + a.sinks + C::rows / a.group + 1;

@@ -89,18 +89,25 @@ __device__ __forceinline__ SeqGeo uniform(SeqGeo g) {
 }
 
 // Sequence of row r (every lane of the wave asks for the same r): the last
-// one that starts at or before it; -1 where no sequence holds the row.
-__device__ __forceinline__ int seq_of_row(const KvArgs &c, int r) {
+// one that starts at or before it; -1 where no sequence holds the row.  g: its
+// geometry, from the same loads.
+__device__ __forceinline__ int seq_of_row(const KvArgs &c, int r, SeqGeo &g) {
   const int lane = threadIdx.x & 63;
-  int below = 0;
-  for (int s0 = 0; s0 <= c.seqs; s0 += 64) {
-    const int s = s0 + lane;
-    const unsigned long long m = __ballot(s <= c.seqs && c.offsets[min(s, c.seqs)] <= r);
-    below += __popcll(m);
+  int found = -1;
+  for (int s0 = 0; s0 < c.seqs; s0 += 64) {
+    const int s = min(s0 + lane, c.seqs - 1);
+    const SeqGeo own = seq_geo(c, s);
+    const unsigned long long m = __ballot(s0 + lane < c.seqs && c.offsets[s] <= r);
+    if (!m) break;
+    const int l = 63 - __clzll((long long)m);
+    found = s0 + l;
+    g.r0 = __builtin_amdgcn_readlane(own.r0, l);
+    g.n = __builtin_amdgcn_readlane(own.n, l);
+    g.pos0 = __builtin_amdgcn_readlane(own.pos0, l);
+    g.len = __builtin_amdgcn_readlane(own.len, l);
     if (m != ~0ull) break;
   }
-  const int s = below - 1;
-  return s >= 0 && s < c.seqs ? s : -1;
+  return found;
 }
 
 // Index of a key's row in the pool, (page * kv_heads + head) * page_size +
