@@ -22,6 +22,7 @@ refuses raises :class:`.binding.MoeError`.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -34,8 +35,9 @@ _CACHE = {"bf16": (B.MOE_BF16, torch.bfloat16, torch.bfloat16),
           # OCP MX-fp8: E4M3 codes and one E8M0 scale byte per 32 elements of head_dim
           "mxfp8": (B.MOE_MXFP8, torch.uint8, torch.bfloat16)}
 _QUANT = {"none": B.MOE_NO_QUANT, "mxfp8": B.MOE_MXFP8, "fp8": B.MOE_FP8}
-# Small calls are bound by the host, so the checks build no message unless they
-# fail, and the stream and device are asked for without torch's wrappers.
+# Small calls are bound by the host: the checks build no message unless they
+# fail, the library's functions are called with plain integers, and the stream
+# and device are asked for without torch's wrappers.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -83,40 +85,49 @@ class RMSNorm:
         _require(quant != "fp8" or 0.0 < fp8_scale < 3.0e38, "fp8 needs a positive fp8_scale")
         _require(eps >= 0.0, "eps must not be negative")
         self.weight, self.eps, self.quant, self.fp8_scale = weight, float(eps), quant, float(fp8_scale)
-        self.hidden = weight.numel()
+        self.hidden, self.dtype = weight.numel(), weight.dtype
         self.device = _device(weight)
         self._q, self._dtype, self._w = _QUANT[quant], _ACT[weight.dtype], weight.data_ptr()
+        self._call = B.lib().moe_rms_norm
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, want_y: bool = True,
                  stream=None) -> NormResult:
         """x, residual: [rows, hidden], rows contiguous inside.  want_y False
         leaves y out where there is an 8-bit output."""
-        w, hidden = self.weight, self.hidden
+        hidden, dev = self.hidden, self.device
         shape = x.shape
         for t in (x,) if residual is None else (x, residual):
-            if t.dim() != 2 or t.shape != shape or shape[1] != hidden or t.dtype != w.dtype or t.device != self.device:
+            if t.dim() != 2 or t.shape != shape or shape[1] != hidden or t.dtype != self.dtype or t.device != dev:
                 raise ValueError("expected [rows, %d] of %s on %s, got %s of %s on %s"
-                                 % (hidden, w.dtype, self.device, list(t.shape), t.dtype, t.device))
+                                 % (hidden, self.dtype, dev, list(t.shape), t.dtype, t.device))
             if t.stride(1) != 1 and hidden != 1:
                 raise ValueError("rows must be contiguous")
-        _require(want_y or self._q != B.MOE_NO_QUANT, "without y there is no output")
-        other = _elsewhere(self.device.index, stream)
+        if not want_y and self._q == B.MOE_NO_QUANT:
+            raise ValueError("without y there is no output")
+        other = _elsewhere(dev.index, stream)
         if other is not None:
             with other:
                 return self(x, residual, want_y=want_y)
         # empty_like of rows that are contiguous inside is contiguous as a whole
-        r = None if residual is None else torch.empty_like(residual)
-        y = torch.empty_like(x) if want_y else None
-        q = scale = None
+        like, r, y, q, scale = torch.empty_like, None, None, None, None
+        rp = rs = ro = yp = qp = sp = 0
+        if residual is not None:
+            r = like(residual)
+            rp, rs, ro = residual.data_ptr(), residual.stride(0), r.data_ptr()
+        if want_y:
+            y = like(x)
+            yp = y.data_ptr()
         if self._q != B.MOE_NO_QUANT:
-            q = torch.empty(shape, dtype=torch.uint8, device=self.device)
+            q = like(x, dtype=torch.uint8)
+            qp = q.data_ptr()
             if self._q == B.MOE_MXFP8:
-                scale = torch.empty((shape[0], hidden // 32), dtype=torch.uint8, device=self.device)
-        B.moe_rms_norm(x.data_ptr(), x.stride(0), None if r is None else residual.data_ptr(),
-                       0 if r is None else residual.stride(0), self._w, self._dtype, shape[0], hidden, self.eps,
-                       None if r is None else r.data_ptr(), None if y is None else y.data_ptr(), self._q,
-                       self.fp8_scale, None if q is None else q.data_ptr(),
-                       None if scale is None else scale.data_ptr(), _raw_stream(self.device.index))
+                n = hidden // 32
+                scale = torch.empty_strided((shape[0], n), (n, 1), dtype=torch.uint8, device=dev)
+                sp = scale.data_ptr()
+        rc = self._call(x.data_ptr(), x.stride(0), rp, rs, self._w, self._dtype, shape[0], hidden, self.eps, ro, yp,
+                        self._q, self.fp8_scale, qp, sp, _raw_stream(dev.index))
+        if rc:
+            B._check(rc)
         return NormResult(r, y, q, scale)
 
 
@@ -147,6 +158,7 @@ class KVBatch:
         self.seqs, self.rows, self.max_rows = seqs, rows, max_rows
         self.c = B.MoeKvBatch(page_table.data_ptr(), row_offsets.data_ptr(), kv_len.data_ptr(), seqs,
                               page_table.shape[1], rows, max_rows)
+        self._ref = ctypes.byref(self.c)
 
 
 class PagedKVCache:
@@ -185,6 +197,10 @@ class PagedKVCache:
         self.dtype, self.device = dtype, _device(k)
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr() if mx else None,
                               vs.data_ptr() if mx else None, num_pages, page_size, kv_heads, head_dim, code)
+        lib = B.lib()
+        self._ref = ctypes.byref(self.c)
+        self._write, self._read = lib.moe_kv_write, lib.moe_kv_read
+        self._attend, self._attend_ws = lib.moe_attention, lib.moe_attention_workspace_bytes
 
     def _check(self, batch, t, heads, what):
         if t.shape != (batch.rows, heads, self.head_dim) or t.dtype != self.act_dtype or t.device != self.device:
@@ -205,8 +221,10 @@ class PagedKVCache:
         if other is not None:
             with other:
                 return self.write(batch, k, v)
-        B.moe_kv_write(self.c, batch.c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                       v.stride(1), _raw_stream(self.device.index))
+        rc = self._write(self._ref, batch._ref, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                         v.stride(1), _raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
 
     def read(self, batch: KVBatch, *, stream=None):
         """The batch's tokens' (k, v) [rows, kv_heads, head_dim], dequantised."""
@@ -217,7 +235,9 @@ class PagedKVCache:
                 return self.read(batch)
         k = torch.empty((batch.rows, self.kv_heads, self.head_dim), dtype=self.act_dtype, device=self.device)
         v = torch.empty_like(k)
-        B.moe_kv_read(self.c, batch.c, k.data_ptr(), v.data_ptr(), _raw_stream(self.device.index))
+        rc = self._read(self._ref, batch._ref, k.data_ptr(), v.data_ptr(), _raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
         return k, v
 
     def attention(self, batch: KVBatch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
@@ -226,12 +246,14 @@ class PagedKVCache:
         its own position; with window > 0 over the last `window` positions and
         the first `sinks`.  heads is a multiple of kv_heads.  scale:
         head_dim ** -0.5 if not given.  A row that sees nothing gives zeros."""
-        _require(q.dim() == 3, "q must be [rows, heads, head_dim]")
+        if q.dim() != 3:
+            raise ValueError("q must be [rows, heads, head_dim]")
         heads = q.shape[1]
         self._check(batch, q, heads, "q")
         if heads == 0 or heads % self.kv_heads:
             raise ValueError("%d heads do not share %d KV heads" % (heads, self.kv_heads))
-        _require(window >= 0 and sinks >= 0, "window and sinks must not be negative")
+        if window < 0 or sinks < 0:
+            raise ValueError("window and sinks must not be negative")
         if out is not None:
             self._check(batch, out, heads, "out")
             _require(out.is_contiguous(), "out must be contiguous")
@@ -242,10 +264,14 @@ class PagedKVCache:
             with other:
                 return self.attention(batch, q, scale, window, sinks, out=out)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        n = B.moe_attention_workspace_bytes(self.c, batch.c, heads, window, sinks)
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-        B.moe_attention(self.c, batch.c, q.data_ptr(), q.stride(0), q.stride(1), heads,
-                        self.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-                        None if ws is None else ws.data_ptr(), n, _raw_stream(self.device.index))
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        n, ws, wp = self._attend_ws(self._ref, batch._ref, heads, window, sinks), None, 0
+        if n:
+            ws = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=self.device)
+            wp = ws.data_ptr()
+        rc = self._attend(self._ref, batch._ref, q.data_ptr(), q.stride(0), q.stride(1), heads,
+                          self.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), wp, n,
+                          _raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
         return out
