@@ -70,19 +70,12 @@ struct Cut {
   }
   // inclusive sums of 64 sequences' weights from s0 on, one a lane
   __device__ __forceinline__ int sums(int s0) const {
-    const int lane = threadIdx.x & 63;
-    int v = weight(s0 + lane);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(v, d, 64);
-      if (lane >= d) v += u;
-    }
-    return v;
+    return wave_scan(weight(s0 + (threadIdx.x & 63)));
   }
   __device__ __forceinline__ int scan(int s0) const { return s0 ? sums(s0) : sums0; }
   __device__ __forceinline__ int total() const {
     int t = 0;
-    for (int s0 = 0; s0 < a.c.seqs; s0 += 64) t += __shfl(scan(s0), 63, 64);
+    for (int s0 = 0; s0 < a.c.seqs; s0 += 64) t += __builtin_amdgcn_readlane(scan(s0), 63);
     return t * a.c.kv_heads;
   }
   // sequence that holds position x, and the position of its first tile
@@ -93,10 +86,10 @@ struct Cut {
       const unsigned long long past = __ballot((t + v) * a.c.kv_heads > x);
       if (past) {
         const int l = __ffsll((long long)past) - 1;
-        start = (t + (l ? __shfl(v, l - 1, 64) : 0)) * a.c.kv_heads;
+        start = (t + (l ? __builtin_amdgcn_readlane(v, l - 1) : 0)) * a.c.kv_heads;
         return s0 + l;
       }
-      t += __shfl(v, 63, 64);
+      t += __builtin_amdgcn_readlane(v, 63);
     }
     return -1;
   }
@@ -105,8 +98,8 @@ struct Cut {
     int t = 0;
     for (int s0 = 0; s0 < a.c.seqs; s0 += 64) {
       const int v = scan(s0);
-      if (s < s0 + 64) return (t + (s > s0 ? __shfl(v, s - s0 - 1, 64) : 0)) * a.c.kv_heads;
-      t += __shfl(v, 63, 64);
+      if (s < s0 + 64) return (t + (s > s0 ? __builtin_amdgcn_readlane(v, s - s0 - 1) : 0)) * a.c.kv_heads;
+      t += __builtin_amdgcn_readlane(v, 63);
     }
     return t * a.c.kv_heads;
   }
@@ -152,25 +145,8 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
     const int h = unit % c.kv_heads, rt0 = unit / c.kv_heads * ROWS;   // first row of the tile
     const int nrows = g.n * a.group;
 
-    // queries: lane l16 holds row rt0 + 16 rt + l16
     i32x4 q[RT][R::q_pieces];
     int lo[RT], hi[RT];
-    static_for<RT>([&](auto rt) MOE_INLINE {
-      const int m = rt0 + 16 * rt + l16;
-      const bool in = m < nrows;
-      const int tok = in ? m / a.group : 0, hq = h * a.group + (in ? m % a.group : 0);
-      const uint8_t *qp = (const uint8_t *)a.q +
-                          ((long long)(g.r0 + tok) * a.q_row + hq * a.q_head) * R::q_elem;
-#pragma unroll
-      for (int p = 0; p < R::q_pieces; ++p) {
-        const int off = F == FMT_MX8 ? HD / 2 * g4 + 16 * p : 64 * p + 16 * g4;
-        q[rt][p] = in ? *(const i32x4 *)(qp + off) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
-      }
-      const RowMask mask(g, tok, in, a.window, a.sinks);
-      hi[rt] = mask.hi;
-      lo[rt] = mask.lo;
-    });
-
     f32x4 o[RT][DT];
     float mx[RT], sum[RT];
 #pragma unroll
@@ -335,8 +311,26 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
     const int tok_a = rt0 / a.group, tok_b = (min(rt0 + ROWS, nrows) - 1) / a.group;
     const int all_hi = min(g.pos0 + tok_a + 1, g.len), all_lo = a.window ? g.pos0 + tok_b - a.window + 1 : 0;
 
-    // in the loop's order: its waits count the loads issued since
     load_pages(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    // queries: lane l16 holds row rt0 + 16 rt + l16
+    static_for<RT>([&](auto rt) MOE_INLINE {
+      const int m = rt0 + 16 * rt + l16;
+      const bool in = m < nrows;
+      const int tok = in ? m / a.group : 0, hq = h * a.group + (in ? m % a.group : 0);
+      const uint8_t *qp = (const uint8_t *)a.q +
+                          ((long long)(g.r0 + tok) * a.q_row + hq * a.q_head) * R::q_elem;
+#pragma unroll
+      for (int p = 0; p < R::q_pieces; ++p) {
+        const int off = F == FMT_MX8 ? HD / 2 * g4 + 16 * p : 64 * p + 16 * g4;
+        q[rt][p] = in ? *(const i32x4 *)(qp + off) ^ (int)a.q_sign : i32x4{0, 0, 0, 0};
+      }
+      const RowMask mask(g, tok, in, a.window, a.sinks);
+      hi[rt] = mask.hi;
+      lo[rt] = mask.lo;
+    });
+
+    // in the loop's order: its waits count the loads issued since
     rows_of(t0);
     load_rows(c.k, c.k_scale, kr, ks);
     __builtin_amdgcn_sched_barrier(0);

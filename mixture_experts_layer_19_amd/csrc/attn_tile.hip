@@ -75,20 +75,15 @@ __device__ __forceinline__ void find_unit(const AttnArgs &a, int u, int &s, int 
     if (lane >= n) rank = lane;
     // lane r: the sequence of rank r
     const int seq = __builtin_amdgcn_ds_permute(rank << 2, lane);
-    int v = __shfl(units, seq, 64);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int w = __shfl_up(v, d, 64);
-      if (lane >= d) v += w;
-    }
+    const int v = wave_scan(__shfl(units, seq, 64));
     const unsigned long long past = __ballot(v > u);
     if (past) {
       const int l = __ffsll((long long)past) - 1;
-      s = s0 + __shfl(seq, l, 64);
-      rt = __shfl(v, l, 64) - 1 - u;               // descending
+      s = s0 + __builtin_amdgcn_readlane(seq, l);
+      rt = __builtin_amdgcn_readlane(v, l) - 1 - u;               // descending
       return;
     }
-    u -= __shfl(v, 63, 64);
+    u -= __builtin_amdgcn_readlane(v, 63);
   }
 }
 

@@ -58,6 +58,18 @@ __device__ __forceinline__ float sum_rows16(float v) {
   return sum_half(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+// Inclusive sums over the lanes of a wave: within rows of 16, then the rows'
+// last lanes carried into the rows behind them.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 to rows 2 and 3
+  return v;
+}
+
 // ----------------------------------------------------------------------------- batch geometry
 
 // One sequence of a batch.  Whatever the device arrays hold, rows stay inside
