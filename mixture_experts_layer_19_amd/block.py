@@ -233,7 +233,9 @@ class PagedKVCache:
         if other is not None:
             with other:
                 return self.read(batch)
-        k = torch.empty((batch.rows, self.kv_heads, self.head_dim), dtype=self.act_dtype, device=self.device)
+        heads, dim = self.kv_heads, self.head_dim
+        k = torch.empty_strided((batch.rows, heads, dim), (heads * dim, dim, 1), dtype=self.act_dtype,
+                                device=self.device)
         v = torch.empty_like(k)
         rc = self._read(self._ref, batch._ref, k.data_ptr(), v.data_ptr(), _raw_stream(self.device.index))
         if rc:

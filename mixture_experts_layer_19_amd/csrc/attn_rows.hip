@@ -104,6 +104,9 @@ struct Cut {
     return t * a.c.kv_heads;
   }
 };
+struct NoCut {
+  __device__ __forceinline__ NoCut(const AttnArgs &) {}
+};
 // The runs: the first `more` of them hold one tile more than the others.
 struct Runs {
   int n, len, more;
@@ -116,8 +119,9 @@ struct Runs {
   }
 };
 
-template <int F, int HD, int RT, int NKH>
-__global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void attn_rows_kernel(AttnArgs a) {
+// WHOLE: a workgroup a unit, nothing is cut (`units` row tiles a sequence).
+template <int F, int HD, int RT, int NKH, bool WHOLE>
+__global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void attn_rows_kernel(AttnArgs a, int units) {
   using C = RowsCfg<F, HD, RT, NKH>;
   using R = typename C::R;
   constexpr int BK = C::BK, ROWS = C::rows, DT = HD / 16;
@@ -128,22 +132,31 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
   float *ml = (float *)(lds + 4 * C::wave_bytes);          // [wave][row] maximum, sum
   const KvArgs &c = a.c;
 
-  const Cut<BK, ROWS> cut(a);
-  const Runs runs(__builtin_amdgcn_readfirstlane(cut.total()), a.grid);
-  const bool idle = (int)blockIdx.x >= runs.n;
-  const int x_begin = idle ? 0 : runs.start(blockIdx.x), x_end = idle ? 0 : runs.start(blockIdx.x + 1);
+  int x_begin = 0, x_end = 1;                              // this workgroup's run of tiles
+  int whole_s = 0, whole_unit = 0;
+  [[maybe_unused]] const std::conditional_t<WHOLE, NoCut, Cut<BK, ROWS>> cut(a);
+  if constexpr (WHOLE) {
+    whole_s = blockIdx.x / (c.kv_heads * units);
+    whole_unit = blockIdx.x % (c.kv_heads * units);
+  } else {
+    const Runs runs(__builtin_amdgcn_readfirstlane(cut.total()), a.grid);
+    const bool idle = (int)blockIdx.x >= runs.n;
+    x_begin = idle ? 0 : runs.start(blockIdx.x);
+    x_end = idle ? 0 : runs.start(blockIdx.x + 1);
+  }
 
   for (int x = x_begin; x < x_end;) {
-    int seq_x;
-    const int s = __builtin_amdgcn_readfirstlane(cut.find(x, seq_x));
+    int s = whole_s, seq_x = 0;
+    if constexpr (!WHOLE) s = __builtin_amdgcn_readfirstlane(cut.find(x, seq_x));
     const SeqGeo g = uniform(seq_geo(c, s));
     const KeyRange<BK> range(g, 0, g.n - 1, a.window, a.sinks);
     const int T = max(range.tiles, 1);
-    const int in_seq = x - __builtin_amdgcn_readfirstlane(seq_x);
-    const int unit = in_seq / T, t0 = in_seq % T;
-    const int t1 = min(T, t0 + (x_end - x));
+    const int in_seq = WHOLE ? 0 : x - __builtin_amdgcn_readfirstlane(seq_x);
+    const int unit = WHOLE ? whole_unit : in_seq / T, t0 = WHOLE ? 0 : in_seq % T;
+    const int t1 = WHOLE ? T : min(T, t0 + (x_end - x));
     const int h = unit % c.kv_heads, rt0 = unit / c.kv_heads * ROWS;   // first row of the tile
     const int nrows = g.n * a.group;
+    if (WHOLE && rt0 >= nrows) break;
 
     i32x4 q[RT][R::q_pieces];
     int lo[RT], hi[RT];
@@ -476,7 +489,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
       }
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == T;
+    const bool whole = WHOLE || (t0 == 0 && t1 == T);
     // a run holds at most two cut units: one it starts inside of, one it ends inside of
     const long long slot = 2ll * blockIdx.x + (x == x_begin ? 0 : 1);
     float *part = a.part + slot * ROWS * (HD + 2);
@@ -624,21 +637,43 @@ struct Launch {
     const long long all = most(c, group);
     return (int)(all >= 0 && all < kRowsGrid ? all : kRowsGrid);
   }
-  static size_t ws(const KvArgs &c, int group) {
-    return (size_t)grid(c, group) * 2 * C::rows * (HD + 2) * sizeof(float);
+  // Up to six tiles a unit (768 keys of bf16 and MX) are not cut: to walk them
+  // costs less than the second launch that joins their pieces (one sequence of
+  // 600 keys: 12.9 us against 14.5; 30 of up to 480: 10.1 against 19.3; one of
+  // 937, eight tiles: 17.6 against 13.9).
+  static bool whole(const AttnArgs &a) {
+    long long tiles = (((long long)a.c.max_pages << a.c.page_shift) + C::BK - 1) / C::BK;
+    if (a.window) {
+      const long long seen = (a.window + (long long)a.c.max_rows - 2) / C::BK + 2 + (a.sinks + C::BK - 1) / C::BK;
+      tiles = tiles < seen ? tiles : seen;
+    }
+    return tiles <= 6;
+  }
+  static bool fits(const AttnArgs &a) { return most(a.c, a.group) >= 0; }
+  static size_t ws(const AttnArgs &a) {
+    return whole(a) ? 0 : (size_t)grid(a.c, a.group) * 2 * C::rows * (HD + 2) * sizeof(float);
+  }
+  template <bool WHOLE>
+  static hipError_t rows(const AttnArgs &a, int u, hipStream_t s) {
+    static const hipError_t once = hipFuncSetAttribute((const void *)attn_rows_kernel<F, HD, RT, NKH, WHOLE>,
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
+    if (once != hipSuccess) return once;
+    attn_rows_kernel<F, HD, RT, NKH, WHOLE><<<a.grid, 256, C::lds, s>>>(a, u);
+    return hipGetLastError();
   }
   static hipError_t run(const AttnArgs &args, hipStream_t s) {
     AttnArgs a = args;
+    const int u = units(a.c, a.group), all = a.c.seqs * a.c.kv_heads * u;
+    if (whole(a)) {
+      a.grid = all;
+      return rows<true>(a, u, s);
+    }
     a.grid = grid(a.c, a.group);
-    static const hipError_t once = hipFuncSetAttribute(
-        (const void *)attn_rows_kernel<F, HD, RT, NKH>, hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
-    if (once != hipSuccess) return once;
-    attn_rows_kernel<F, HD, RT, NKH><<<a.grid, 256, C::lds, s>>>(a);
-    const int u = units(a.c, a.group);
+    const hipError_t err = rows<false>(a, u, s);
+    if (err != hipSuccess) return err;
     // rows of a unit, at most
     const long long rows = (long long)a.c.max_rows * a.group;
     const int unit_rows = (int)(rows < C::rows ? rows : C::rows);
-    const long long all = (long long)a.c.seqs * a.c.kv_heads * u;
     const int per = all < 256 ? 1 : 1024 / HD;
     attn_join_kernel<F, HD, RT, NKH><<<(unsigned)(all * ((unit_rows + per - 1) / per)), 256, 0, s>>>(a, unit_rows, u, per);
     return hipGetLastError();
@@ -668,7 +703,10 @@ auto pick(const KvArgs &c, int group, Fn &&f) {
 }  // namespace
 
 size_t attn_rows_ws_bytes(const AttnArgs &a) {
-  return pick(a.c, a.group, [&](auto l) -> size_t { return l.most(a.c, a.group) < 0 ? 0 : l.ws(a.c, a.group); });
+  return pick(a.c, a.group, [&](auto l) { return l.ws(a); });
+}
+bool attn_rows_fits(const AttnArgs &a) {
+  return pick(a.c, a.group, [&](auto l) { return l.fits(a); });
 }
 hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t s) {
   return pick(a.c, a.group, [&](auto l) { return l.run(a, s); });

@@ -162,7 +162,7 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   if (!q || !out || !al(q, 16) || !al(out, 16) || !al(ws, 16) || !strides_ok(a.c, q_row, q_head))
     return MOE_ERR_INVALID_ARG;
   const size_t need = workspace(a);
-  if (few_rows(a) ? need == 0 : !attn_tile_fits(a)) return MOE_ERR_UNSUPPORTED;
+  if (!(few_rows(a) ? attn_rows_fits(a) : attn_tile_fits(a))) return MOE_ERR_UNSUPPORTED;
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   a.q = q;
   a.q_row = q_row;

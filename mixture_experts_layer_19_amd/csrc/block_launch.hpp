@@ -50,11 +50,11 @@ struct AttnArgs {
   int grid;                    // workgroups of the launch
 };
 // Few query rows a sequence (attn_rows.hip), and many (attn_tile.hip).
-// Workspace bytes first;
-// 0: too large a batch for the kernels' 32-bit counts.
+// Workspace bytes (0: none needed); whether the batch is within the kernels'
+// 32-bit counts.
 size_t attn_rows_ws_bytes(const AttnArgs &a);
+bool attn_rows_fits(const AttnArgs &a);
 hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream);
-// (0: needs none)
 size_t attn_tile_ws_bytes(const AttnArgs &a);
 bool attn_tile_fits(const AttnArgs &a);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t stream);

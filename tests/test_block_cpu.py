@@ -91,6 +91,8 @@ def test_operand_refusals(B):
                dict(heads=3), dict(heads=0), dict(window=-1), dict(sinks=-1), dict(scale=float("nan")),
                dict(scale=float("inf"))):
         refused(B, inv, B.moe_attention, c, b, *dict(ok, **kw).values())
+    assert B.moe_attention_workspace_bytes(c, b, 4, 0, 0) == 0         # a short context needs none
+    b = batch(B, max_pages=200)
     n = B.moe_attention_workspace_bytes(c, b, 4, 0, 0)
     assert n > 0
     refused(B, B.MOE_ERR_WORKSPACE, B.moe_attention, c, b, *dict(ok, n=n - 1).values())
