@@ -258,6 +258,19 @@ MOE_API moe_status moe_layer_forward(moe_ctx *ctx, const moe_desc *desc /* host 
                              const moe_weights *w /* host */, const void *x, int32_t T, void *out,
                              void *ws, size_t ws_bytes, void *stream);
 
+/* moe_layer_forward with x also given as codes of the experts' activation
+ * format, as moe_rms_norm writes them beside y, so that the experts read those
+ * and x is not quantised again: xq [T,H] E4M3; xq_scale [T,H/32] E8M0 for
+ * MX-fp8 and MXFP4 experts, NULL for FP8 ones (whose codes are of
+ * x / fp8_x_scale).  Gating reads x, as it does without them.  Both arrays
+ * 16-byte aligned.  Layers of f32 or bf16 experts return
+ * MOE_ERR_UNSUPPORTED.  Given the codes that moe_layer_forward makes
+ * (moe_mx_quantize, moe_fp8_quantize) the result is the same bit for bit. */
+MOE_API moe_status moe_layer_forward_quantized(moe_ctx *ctx, const moe_desc *desc /* host */,
+                             const moe_weights *w /* host */, const void *x, const uint8_t *xq,
+                             const uint8_t *xq_scale, int32_t T, void *out, void *ws,
+                             size_t ws_bytes, void *stream);
+
 /* Per-stage timing of moe_layer_forward.  With profiling enabled the call
  * records a pair of timing events around each stage on the stream the stage
  * runs on; moe_ctx_stage_ms then waits for the last call's events and writes

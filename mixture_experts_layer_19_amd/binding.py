@@ -25,7 +25,7 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_status_string", "moe_ctx_la
            "moe_fp8_quantize",
            "moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_ws_topk", "moe_ctx_set_profiling", "moe_ctx_stage_ms",
-           "moe_layer_forward_noalloc",
+           "moe_layer_forward_quantized", "moe_layer_forward_noalloc",
            "moe_rms_norm", "moe_kv_write", "moe_kv_read", "moe_attention_workspace_bytes",
            "moe_attention")
 MOE_NO_QUANT = -1
@@ -99,6 +99,7 @@ def lib():
             "moe_grouped_ffn": ([P, DP, WP, ctypes.c_int, P, I32, P, P, P, P, S, P], ctypes.c_int),
             "moe_combine": ([P, DP, P, P, P, P, I32, P, P], ctypes.c_int),
             "moe_layer_forward": ([P, DP, WP, P, I32, P, P, S, P], ctypes.c_int),
+            "moe_layer_forward_quantized": ([P, DP, WP, P, P, P, I32, P, P, S, P], ctypes.c_int),
             "moe_layer_forward_noalloc": ([P, DP, WP, P, I32, P, P], ctypes.c_int),
             "moe_layer_ws_topk": ([DP, I32, ctypes.POINTER(S), ctypes.POINTER(S)], ctypes.c_int),
             "moe_ctx_set_profiling": ([P, ctypes.c_int], ctypes.c_int),
@@ -215,6 +216,12 @@ def moe_combine(ctx, desc, y, dest, topk_w, shared_out, T, out, stream=None):
 def moe_layer_forward(ctx, desc, weights, x, T, out, ws, ws_bytes, stream=None):
     _check(lib().moe_layer_forward(ctx, ctypes.byref(desc), ctypes.byref(weights), _ptr(x), T,
                                    _ptr(out), _ptr(ws), ws_bytes, _stream(stream)), ctx)
+
+
+def moe_layer_forward_quantized(ctx, desc, weights, x, xq, xq_scale, T, out, ws, ws_bytes, stream=None):
+    _check(lib().moe_layer_forward_quantized(ctx, ctypes.byref(desc), ctypes.byref(weights), _ptr(x), _ptr(xq),
+                                             _ptr(xq_scale), T, _ptr(out), _ptr(ws), ws_bytes,
+                                             _stream(stream)), ctx)
 
 
 def moe_layer_forward_noalloc(ctx, desc, weights, x, T, out, stream=None):

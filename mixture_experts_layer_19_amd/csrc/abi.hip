@@ -613,9 +613,11 @@ moe_status moe_layer_ws_topk(const moe_desc *desc, int32_t T, size_t *idx_offset
   return MOE_OK;
 }
 
-moe_status moe_layer_forward(moe_ctx *ctx, const moe_desc *desc, const moe_weights *w,
-                             const void *x, int32_t T, void *out, void *ws, size_t ws_bytes,
-                             void *stream) {
+// The layer; xq, xq_scale: x as codes of the expert format (moe_layer_forward_quantized),
+// or null, then they are made here.
+static moe_status layer_forward(moe_ctx *ctx, const moe_desc *desc, const moe_weights *w,
+                                const void *x, const uint8_t *xq, const uint8_t *xq_scale, int32_t T,
+                                void *out, void *ws, size_t ws_bytes, void *stream) {
   moe_status st = check_desc(desc);
   if (st != MOE_OK) return st;
   if ((st = check_ctx(ctx)) != MOE_OK) return st;
@@ -647,7 +649,10 @@ moe_status moe_layer_forward(moe_ctx *ctx, const moe_desc *desc, const moe_weigh
 
   const void *xa = x;
   const uint8_t *xs = nullptr;
-  if (mx) {
+  if (xq) {
+    xa = xq;
+    xs = xq_scale;
+  } else if (mx) {
     // the expert-format activations feed both the shared and the routed experts
     MOE_TRY(tm.start(MOE_STAGE_MX_QUANT, s), "timing");
     MOE_TRY(launch_mx_quantize(x, 1, T, H, (uint8_t *)b + L.xq, (uint8_t *)b + L.xs, s),
@@ -745,6 +750,23 @@ moe_status moe_layer_forward(moe_ctx *ctx, const moe_desc *desc, const moe_weigh
   MOE_TRY(tm.stop(MOE_STAGE_COMBINE, s), "timing");
 #undef MOE_TRY
   return MOE_OK;
+}
+
+moe_status moe_layer_forward(moe_ctx *ctx, const moe_desc *desc, const moe_weights *w,
+                             const void *x, int32_t T, void *out, void *ws, size_t ws_bytes,
+                             void *stream) {
+  return layer_forward(ctx, desc, w, x, nullptr, nullptr, T, out, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_forward_quantized(moe_ctx *ctx, const moe_desc *desc, const moe_weights *w,
+                                       const void *x, const uint8_t *xq, const uint8_t *xq_scale,
+                                       int32_t T, void *out, void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (!mx_act(desc) && !fp8_act(desc)) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!xq || !al16(xq) || !xq_scale != !mx_act(desc) || !al16(xq_scale)))
+    return MOE_ERR_INVALID_ARG;
+  return layer_forward(ctx, desc, w, x, xq, xq_scale, T, out, ws, ws_bytes, stream);
 }
 
 moe_status moe_layer_forward_noalloc(moe_ctx *ctx, const moe_desc *desc, const moe_weights *w,

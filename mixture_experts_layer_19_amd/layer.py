@@ -124,13 +124,25 @@ class DeviceLayer:
     def out_dtype(self):
         return torch_dtype(self.desc.out_dtype)
 
-    def forward(self, x: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, out: torch.Tensor = None, stream=None, codes=None) -> torch.Tensor:
+        """codes: (q, scale) of x in the experts' 8-bit format, as
+        :class:`.block.RMSNorm` gives them (scale None for static FP8); the
+        experts then read those instead of quantising x again."""
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.w.H), dtype=self.out_dtype(), device=self.dev)
         ws = self.workspace(T)
         s = stream if stream is not None else torch.cuda.current_stream(self.dev)
-        B.moe_layer_forward(self.ctx, self.desc, self.weights, x, T, out, ws, ws.numel(), s)
+        if codes is None:
+            B.moe_layer_forward(self.ctx, self.desc, self.weights, x, T, out, ws, ws.numel(), s)
+            return out
+        q, scale = codes
+        for t, want in ((q, (T, self.w.H)), (scale, (T, self.w.H // 32))):
+            if t is not None and (tuple(t.shape) != want or t.dtype != torch.uint8 or not t.is_contiguous()
+                                  or t.device != x.device):
+                raise ValueError("codes must be contiguous uint8 %s on %s, got %s %s on %s"
+                                 % (list(want), x.device, t.dtype, list(t.shape), t.device))
+        B.moe_layer_forward_quantized(self.ctx, self.desc, self.weights, x, q, scale, T, out, ws, ws.numel(), s)
         return out
 
     def capture(self, x: torch.Tensor, out: torch.Tensor):
