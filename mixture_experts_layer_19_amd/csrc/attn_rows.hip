@@ -44,14 +44,20 @@ struct RowsCfg {
   static constexpr int o_pitch = HD * 4 + 16, o_bytes = rows * o_pitch;
   static constexpr int wave_bytes = v_bytes > o_bytes ? v_bytes : o_bytes;
   static constexpr int lds = 4 * wave_bytes + 4 * rows * 8;
+  // Cost of a unit, in tiles (Cut).  MX-fp8, 64 sequences of up to 8100 keys: 0
+  // 122, 1 114, 2 115, 4 117 us; at head_dim 64: 74, 65, 63, 65; 32 sequences of 4
+  // tokens (RT = 2): 80, 78, 71, 72; bf16, 64 sequences: 207, 202, 204, 210.
+  static constexpr int unit_cost = RT == 2 || BK * R::bytes <= 8192 ? 2 : 1;
   // two workgroups a CU where the registers suffice: the one's loads run under
   // the other's products
   static constexpr int occupancy = RT == 1 && HD <= 128 ? 2 : 1;
 };
 
 // The even cut of the tiles of all units.  Unit order: sequence, row tile,
-// KV head.  Every row tile of a sequence counts the sequence's tiles.
-template <int BK, int ROWS>
+// KV head.  Every row tile of a sequence counts the sequence's tiles and, ahead
+// of them, COST positions for what a unit costs beside them (lookups, the merge
+// of its waves): a run of many short units would end last otherwise.
+template <int BK, int ROWS, int COST>
 struct Cut {
   const AttnArgs &a;
   int sums0;                   // scan(0)
@@ -66,7 +72,7 @@ struct Cut {
   __device__ __forceinline__ int weight(int s) const {
     if (s >= a.c.seqs) return 0;
     const SeqGeo g = seq_geo(a.c, s);
-    return g.n ? row_tiles(a, g) * tiles(a, g) : 0;
+    return g.n ? row_tiles(a, g) * (tiles(a, g) + COST) : 0;
   }
   // inclusive sums of 64 sequences' weights from s0 on, one a lane
   __device__ __forceinline__ int sums(int s0) const {
@@ -124,7 +130,7 @@ template <int F, int HD, int RT, int NKH, bool WHOLE>
 __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void attn_rows_kernel(AttnArgs a, int units) {
   using C = RowsCfg<F, HD, RT, NKH>;
   using R = typename C::R;
-  constexpr int BK = C::BK, ROWS = C::rows, DT = HD / 16;
+  constexpr int BK = C::BK, ROWS = C::rows, COST = C::unit_cost, DT = HD / 16;
   extern __shared__ __align__(16) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -134,7 +140,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
 
   int x_begin = 0, x_end = 1;                              // this workgroup's run of tiles
   int whole_s = 0, whole_unit = 0;
-  [[maybe_unused]] const std::conditional_t<WHOLE, NoCut, Cut<BK, ROWS>> cut(a);
+  [[maybe_unused]] const std::conditional_t<WHOLE, NoCut, Cut<BK, ROWS, COST>> cut(a);
   if constexpr (WHOLE) {
     whole_s = blockIdx.x / (c.kv_heads * units);
     whole_unit = blockIdx.x % (c.kv_heads * units);
@@ -152,8 +158,10 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
     const KeyRange<BK> range(g, 0, g.n - 1, a.window, a.sinks);
     const int T = max(range.tiles, 1);
     const int in_seq = WHOLE ? 0 : x - __builtin_amdgcn_readfirstlane(seq_x);
-    const int unit = WHOLE ? whole_unit : in_seq / T, t0 = WHOLE ? 0 : in_seq % T;
-    const int t1 = WHOLE ? T : min(T, t0 + (x_end - x));
+    const int unit = WHOLE ? whole_unit : in_seq / (T + COST), at = WHOLE ? COST : in_seq % (T + COST);
+    const int x_next = WHOLE ? x_end : min(x_end, x + (T + COST - at));
+    const int t0 = max(at - COST, 0), t1 = WHOLE ? T : at + (x_next - x) - COST;
+    if (t1 <= t0) break;                           // the run ends before the unit's tiles
     const int h = unit % c.kv_heads, rt0 = unit / c.kv_heads * ROWS;   // first row of the tile
     const int nrows = g.n * a.group;
     if (WHOLE && rt0 >= nrows) break;
@@ -525,7 +533,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
       }
     }
     __syncthreads();
-    x += t1 - t0;
+    x = x_next;
   }
   clear_free_rows<F, HD>(a);
 }
@@ -537,7 +545,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
 template <int F, int HD, int RT, int NKH>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit_rows, int units, int per) {
   using C = RowsCfg<F, HD, RT, NKH>;
-  constexpr int BK = C::BK, ROWS = C::rows;
+  constexpr int BK = C::BK, ROWS = C::rows, COST = C::unit_cost;
   constexpr int COLS = HD / 4, SL = 256 / COLS;
   __shared__ f32x4 red[256];
   __shared__ float redm[SL][2];
@@ -547,16 +555,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit_row
   const int unit = blockIdx.x / parts, h = unit % c.kv_heads;
   const int s = unit / c.kv_heads / units, rt = unit / c.kv_heads % units;
   const int m = blockIdx.x % parts * per + (per == 1 ? 0 : sl);
-  const Cut<BK, ROWS> cut(a);
+  const Cut<BK, ROWS, COST> cut(a);
   const SeqGeo g = uniform(seq_geo(c, s));
   const int nrows = g.n * a.group - rt * ROWS;      // of this unit
   if (nrows <= 0) return;
   const Runs runs(__builtin_amdgcn_readfirstlane(cut.total()), a.grid);
-  const int T = Cut<BK, ROWS>::tiles(a, g);
-  const int x0 = __builtin_amdgcn_readfirstlane(cut.first(s)) + (rt * c.kv_heads + h) * T;
-  const int w0 = runs.of(x0), w1 = runs.of(x0 + T - 1);
+  const int T = Cut<BK, ROWS, COST>::tiles(a, g);
+  const int x0 = __builtin_amdgcn_readfirstlane(cut.first(s)) + (rt * c.kv_heads + h) * (T + COST);
+  const int w0 = runs.of(x0 + COST), w1 = runs.of(x0 + COST + T - 1);
   if (w0 == w1) return;                            // never cut: its workgroup wrote it
-  const int first_slot = 2 * w0 + (runs.start(w0) == x0 ? 0 : 1);
+  const int first_slot = 2 * w0 + (runs.start(w0) >= x0 ? 0 : 1);
   const bool in = m < min(nrows, ROWS) && m < unit_rows;
   const int mr = in ? m : 0;
   float top = kNegBig, l = 0.0f;
@@ -627,7 +635,7 @@ struct Launch {
   }
   // tiles of all units, at most; -1 past 32 bits, which the kernels count in
   static long long most(const KvArgs &c, int group) {
-    const long long tiles = (((long long)c.max_pages << c.page_shift) + C::BK - 1) / C::BK + 1;
+    const long long tiles = (((long long)c.max_pages << c.page_shift) + C::BK - 1) / C::BK + 1 + C::unit_cost;
     const long long sums = tiles * units(c, group);
     if (sums > INT32_MAX) return -1;
     const long long seq = sums * c.kv_heads;
