@@ -14,9 +14,9 @@
 // and the values of the last (step, below).
 //
 // K and V tiles come through registers (MX codes become bf16 there, exactly)
-// into two LDS buffers each, with one barrier a tile.  Rows are XOR-swizzled in
-// 16-byte chunks so that both reads, K's by rows and V's transposed, spread
-// over the banks (no conflicts counted).
+// into two LDS buffers each, with one barrier a tile.  Rows are longer than
+// their data, so that the reads, K's by rows and V's transposed, spread over the
+// banks (TileCfg), and every read's address is one register and a constant.
 //
 // The running maximum is a reference that moves only when a score passes it
 // by 2^8: the weights stay below 2^8 of fp32 and the output is rescaled rarely.
@@ -33,22 +33,21 @@ struct TileCfg {
   static constexpr int BK = 64;                            // keys of a tile
   static constexpr int elem = F == FMT_F32 ? 4 : 2;        // in LDS
   static constexpr int row_bytes = HD * elem, chunks = row_bytes / 16;
-  static constexpr int tile = BK * row_bytes;              // K or V
-  static constexpr int lds = 4 * tile + 8 * NW;
+  // Rows in LDS.  Of K, 16 lanes read 16 bytes each of 16 rows: 4 banks further a
+  // row.  Of V, 32 lanes read 64 bytes each of 4 rows: 16 banks further a row (no
+  // conflicts counted).  fp32 reads 128 bytes each of 2 rows of V that share
+  // their banks: 84 us for the mixed batch, and 90 with rows 32 bytes longer.
+  static constexpr int k_pitch = row_bytes + 16, v_pitch = row_bytes + (F == FMT_F32 ? 0 : 64);
+  static constexpr int k_tile = BK * k_pitch, v_tile = BK * v_pitch;
+  static constexpr int lds = 2 * (k_tile + v_tile) + 8 * NW;
   // staging of K or V, pieces of 16 bytes a thread: bf16 and fp32 by chunk, MX
   // 16 codes or more of one key (parts threads a key; threads beyond them do
   // what others do)
   static constexpr int parts = HD / 16 < NW ? HD / 16 : NW, codes = HD / parts, scales = codes > 32 ? codes / 32 : 1;
-  static constexpr int pieces = F == FMT_MX8 ? codes / 16 : tile / 16 / threads;
+  static constexpr int pieces = F == FMT_MX8 ? codes / 16 : BK * row_bytes / 16 / threads;
   static constexpr int span = F == FMT_MX8 ? 1 : 64 / chunks;   // keys of a wave's piece (of one page)
   static constexpr int QP = row_bytes / 32;                // 16-byte query pieces a lane
   static constexpr int DT = HD / 32;
-  // chunk c of key row r is stored at chunk c ^ swz(r)
-  __device__ __forceinline__ static int swz(int r) {
-    if constexpr (F == FMT_F32) return (r & 7) ^ (((r >> 2) & 1) << 3);
-    else if constexpr (HD == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    else return ((r & 3) << 2) | ((r >> 2) & 3);
-  }
 };
 
 // Sequence and row tile of unit u, or s = -1 past the last unit.  Long units
@@ -93,7 +92,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
   constexpr int ROWS = C::rows, BK = C::BK, DT = C::DT, QP = C::QP, NP = C::pieces;
   constexpr int KEYS = F == FMT_MX8 ? 1 : NP;              // places that a thread stages pieces from
   extern __shared__ __align__(16) uint8_t lds[];           // K0 K1 V0 V1, flags
-  int *flags = (int *)(lds + 4 * C::tile);                 // [stage][wave]
+  int *flags = (int *)(lds + 2 * (C::k_tile + C::v_tile));   // [stage][wave]
   const int tid = threadIdx.x, lane = tid & 63, q32 = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const KvArgs &c = a.c;
@@ -194,11 +193,11 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     }
   };
   // (`finite`: zeros in place of what is not)
-  auto put = [&](const Stage &st, uint8_t *tile, auto finite) MOE_INLINE {
+  auto put = [&](const Stage &st, uint8_t *tile, int pitch, auto finite) MOE_INLINE {
     auto chunk = [&](int key, int ch, uint4 w) MOE_INLINE {
       if constexpr (finite)
         w = make_uint4(word_finite<F>(w.x), word_finite<F>(w.y), word_finite<F>(w.z), word_finite<F>(w.w));
-      *(uint4 *)(tile + key * C::row_bytes + ((ch ^ C::swz(key)) << 4)) = w;
+      *(uint4 *)(tile + key * pitch + (ch << 4)) = w;
     };
     if constexpr (F == FMT_MX8) {
 #pragma unroll
@@ -220,8 +219,8 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     const int k0 = range.key(t);
     return k0 + BK <= all_hi && k0 >= all_lo && have == ~0ull;
   };
-  auto k_tile = [&](int t) MOE_INLINE { return lds + ((t - t0) & 1) * C::tile; };
-  auto v_tile = [&](int t) MOE_INLINE { return lds + (2 + ((t - t0) & 1)) * C::tile; };
+  auto k_tile = [&](int t) MOE_INLINE { return lds + ((t - t0) & 1) * C::k_tile; };
+  auto v_tile = [&](int t) MOE_INLINE { return lds + 2 * C::k_tile + ((t - t0) & 1) * C::v_tile; };
   auto store_v = [&](Stage &st, int t, unsigned long long have) MOE_INLINE {
     if (have != ~0ull) {                                   // V of keys that do not exist: zeros
 #pragma unroll
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
         }
     }
     if (!plain(t, have)) {
-      put(st, v_tile(t), std::true_type{});
+      put(st, v_tile(t), C::v_pitch, std::true_type{});
       bool bad = false;
       if constexpr (F == FMT_MX8)
 #pragma unroll
@@ -245,38 +244,22 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       const unsigned long long any = __ballot(bad);
       if (lane == 0) flags[NW * ((t - t0) & 1) + wave] = any != 0;
     } else {
-      put(st, v_tile(t), std::false_type{});
+      put(st, v_tile(t), C::v_pitch, std::false_type{});
     }
   };
 
-  // ---- products, of halves of a tile (32 keys).  Addresses within LDS: the
-  // swizzle makes a lane's reads XORs and offsets of its first.  K: lane q32
-  // reads key row q32 of a half, chunk 2 p + hf.
-  // The buffers of the next tile are an XOR away, too (tile is a power of two).
-  static_assert((C::tile & (C::tile - 1)) == 0, "buffers differ in one bit");
+  // ---- products, of halves of a tile (32 keys).  Addresses within LDS of the
+  // lane's first reads; the first V buffer that is read is that of the tile
+  // before the first.
   const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t *)lds;
-  uint32_t k_addr[QP], v_addr[F == FMT_F32 ? 4 * DT : 2 * DT];
-  {
-    const uint32_t k0 = q32 * C::row_bytes + ((hf ^ C::swz(q32)) << 4);
-    const uint32_t v0 =
-        F == FMT_F32 ? 4 * hf * C::row_bytes + (((q32 >> 2) ^ C::swz(4 * hf)) << 4) + 4 * (q32 & 3)
-                     : (4 * hf + ((lane & 15) >> 2)) * C::row_bytes + 8 * (lane & 1) +
-                           (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ C::swz(4 * hf + ((lane & 15) >> 2))) << 4);
-#pragma unroll
-    for (int p = 0; p < QP; ++p) k_addr[p] = lds0 + (k0 ^ (32 * p));
-    // the first V buffer that is read is that of the tile before the first
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int x = 0; x < (F == FMT_F32 ? 4 : 2); ++x)
-        v_addr[(F == FMT_F32 ? 4 : 2) * d + x] =
-            lds0 + 3 * C::tile + (F == FMT_F32 ? v0 ^ (128 * d) ^ (16 * x) : v0 ^ (64 * d) ^ (32 * x));
-  }
+  uint32_t k_addr = lds0 + q32 * C::k_pitch + 16 * hf;
+  uint32_t v_addr = lds0 + 2 * C::k_tile + C::v_tile +
+                    (F == FMT_F32 ? 4 * hf * C::v_pitch + 4 * q32
+                                  : (4 * hf + ((lane & 15) >> 2)) * C::v_pitch + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
+  const uint32_t k_both = 2 * k_addr + C::k_tile, v_both = 2 * v_addr - C::v_tile;
   auto other_buffers = [&]() MOE_INLINE {
-#pragma unroll
-    for (auto &x : k_addr) x ^= C::tile;
-#pragma unroll
-    for (auto &x : v_addr) x ^= C::tile;
+    k_addr = k_both - k_addr;
+    v_addr = v_both - v_addr;
   };
   // The products of a step, in slots: even ones a piece of the scores' head_dim
   // (S^T; element i is key 8 (i / 4) + 4 hf + i % 4 of the half), odd ones 16
@@ -288,7 +271,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
   using Weights = std::conditional_t<F == FMT_F32, f32x16, i32x8>;
   auto read_k = [&](auto n, int half) MOE_INLINE {
     using P = const __attribute__((address_space(3))) i32x4 *;
-    return *(P)(size_t)(k_addr[n] + 32 * half * C::row_bytes);
+    return *(P)(size_t)(k_addr + 32 * half * C::k_pitch + 32 * n);
   };
   auto read_v = [&](auto n, int half) MOE_INLINE {
     constexpr int dt = n % DT, part = n / DT;
@@ -297,14 +280,14 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       using P = const __attribute__((address_space(3))) int *;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        f[i] = *(P)(size_t)(v_addr[4 * dt + i] + (32 * half + 8 * part + i) * C::row_bytes);
+        f[i] = *(P)(size_t)(v_addr + (32 * half + 8 * part + i) * C::v_pitch + 128 * dt);
     } else {
       // a group of 16 lanes reads 4 keys x 16 columns, transposed
       using P = __attribute__((address_space(3))) s16x4 *;
       const i32x2 v0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (P)(size_t)(v_addr[2 * dt] + (32 * half + 16 * part) * C::row_bytes)));
+          (P)(size_t)(v_addr + (32 * half + 16 * part) * C::v_pitch + 64 * dt)));
       const i32x2 v1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (P)(size_t)(v_addr[2 * dt + 1] + (32 * half + 16 * part + 8) * C::row_bytes)));
+          (P)(size_t)(v_addr + (32 * half + 16 * part + 8) * C::v_pitch + 64 * dt)));
       f = __builtin_shufflevector(v0, v1, 0, 1, 2, 3);
     }
     return f;
@@ -450,13 +433,13 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       load_tile(s0, c.k, c.k_scale, row);
       load_tile(sv, c.v, c.v_scale, row);
       load_tile(sk, c.k, c.k_scale, row1);
-      put(s0, k_tile(t0), std::false_type{});
+      put(s0, k_tile(t0), C::k_pitch, std::false_type{});
       store_v(sv, t0, row.have);
-      put(sk, k_tile(t0 + 1), std::false_type{});
+      put(sk, k_tile(t0 + 1), C::k_pitch, std::false_type{});
     }
     Pages page = pages_of(t0 + 2);
-    for (int i = tid; i < 32 * C::chunks; i += C::threads)
-      *(uint4 *)(v_tile(t0 + 1) + 32 * C::row_bytes + 16 * i) = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 32 * C::v_pitch / 16; i += C::threads)
+      *(uint4 *)(v_tile(t0 + 1) + 32 * C::v_pitch + 16 * i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     f32x16 sa, sb;
     Weights wa, wb;
@@ -484,7 +467,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       }
       row = row1;
       row1 = row2;
-      put(sk, k_tile(t + 2), std::false_type{});
+      put(sk, k_tile(t + 2), C::k_pitch, std::false_type{});
       last_plain = is_plain;
       if (t + 1 < t1) {
         is_plain = plain(t + 1, row.have);
