@@ -557,7 +557,7 @@ struct TileLaunch {
     const long long all = (long long)a.c.rows * a.group / C::rows + a.c.seqs;
     return each < all ? each : all;
   }
-  // Enough workgroups for every CU (two of four waves where they fit), but four
+  // Enough workgroups for every CU (OCC of four waves), but four
   // key tiles at least in a run where the longest possible row sees that many.
   // fp32 of head_dim 64 is bound by its slow matrix instructions and by uneven
   // units: twice as many (12 sequences of 1-211 tokens over up to 900 keys, 16
@@ -594,15 +594,19 @@ struct TileLaunch {
   }
 };
 
+// Waves a workgroup and workgroups of four waves a CU: as many as the registers
+// hold.  head_dim 64 at three (bf16 8 registers short, kept in memory) against
+// two: chunks of 640-1408 tokens over up to 7501 keys 562 and 598 us, a window
+// of 1024 129 and 147; one of eight waves: 606.
 template <typename Fn>
 auto pick_tile(const KvArgs &c, Fn &&f) {
   if (c.fmt == FMT_F32) return c.head_dim == 64 ? f(TileLaunch<FMT_F32, 64, 4, 2>{}) : f(TileLaunch<FMT_F32, 128, 4, 1>{});
   if (c.fmt == FMT_BF16) {
-    if (c.head_dim == 64) return f(TileLaunch<FMT_BF16, 64, 4, 2>{});
+    if (c.head_dim == 64) return f(TileLaunch<FMT_BF16, 64, 4, 3>{});
     if (c.head_dim == 128) return f(TileLaunch<FMT_BF16, 128, 8, 2>{});
     return f(TileLaunch<FMT_BF16, 256, 4, 1>{});
   }
-  if (c.head_dim == 64) return f(TileLaunch<FMT_MX8, 64, 4, 2>{});
+  if (c.head_dim == 64) return f(TileLaunch<FMT_MX8, 64, 4, 3>{});
   if (c.head_dim == 128) return f(TileLaunch<FMT_MX8, 128, 8, 2>{});
   return f(TileLaunch<FMT_MX8, 256, 4, 1>{});
 }
