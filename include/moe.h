@@ -323,7 +323,7 @@ MOE_API moe_status moe_layer_forward_noalloc(moe_ctx *ctx, const moe_desc *desc 
 /* RMS norm with the residual's addition and an output in 8 bits:
  *
  *   s = x + residual                               (fp32; s = x if NULL)
- *   y = s / sqrt(mean(s^2) + eps) * weight         (fp32, from the unrounded s)
+ *   y = s / sqrt(mean(s^2) + eps) * weight         (64 bits, from the unrounded s)
  *   residual_out = s, y_out = y                    (rounded once to `dtype`)
  *   q: codes of the unrounded y
  *

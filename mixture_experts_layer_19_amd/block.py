@@ -72,8 +72,8 @@ class RMSNorm:
     """y = (x + residual) / sqrt(mean((x + residual)^2) + eps) * weight.
 
     quant: "none"; "mxfp8", E4M3 codes with an E8M0 scale byte per 32 elements;
-    "fp8", E4M3 codes of y / fp8_scale.  The statistics and the codes come from
-    fp32 values; every output is rounded once."""
+    "fp8", E4M3 codes of y / fp8_scale.  The sum is held in fp32, the statistics
+    and y in 64 bits; every output is rounded once from them."""
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-5, quant: str = "none",
                  fp8_scale: float = 0.0):
