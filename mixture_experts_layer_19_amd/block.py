@@ -48,6 +48,16 @@ def _require(ok, what):
         raise ValueError(what)
 
 
+def _bound(name):
+    """An attribute whose address the C structs hold: its contents may change in
+    place, another tensor needs another object."""
+    def keep(self, value):
+        if value is not self.__dict__[name]:
+            raise AttributeError("%s is changed in place, not replaced" % name)
+
+    return property(lambda self: self.__dict__[name], keep)
+
+
 def _elsewhere(index, stream):
     """A context in which the current device and stream are the call's, or None
     if they are already."""
@@ -75,6 +85,8 @@ class RMSNorm:
     "fp8", E4M3 codes of y / fp8_scale.  The sum is held in fp32, the statistics
     and y in 64 bits; every output is rounded once from them."""
 
+    weight = _bound("weight")
+
     def __init__(self, weight: torch.Tensor, eps: float = 1e-5, quant: str = "none",
                  fp8_scale: float = 0.0):
         _require(weight.dim() == 1 and weight.is_contiguous() and weight.numel() > 0,
@@ -84,10 +96,11 @@ class RMSNorm:
         _require(quant != "mxfp8" or weight.numel() % 32 == 0, "mxfp8 needs a hidden size in multiples of 32")
         _require(quant != "fp8" or 0.0 < fp8_scale < 3.0e38, "fp8 needs a positive fp8_scale")
         _require(eps >= 0.0, "eps must not be negative")
-        self.weight, self.eps, self.quant, self.fp8_scale = weight, float(eps), quant, float(fp8_scale)
+        self.__dict__["weight"] = weight
+        self.eps, self.quant, self.fp8_scale = float(eps), quant, float(fp8_scale)
         self.hidden, self.dtype = weight.numel(), weight.dtype
         self.device = _device(weight)
-        self._q, self._dtype, self._w = _QUANT[quant], _ACT[weight.dtype], weight.data_ptr()
+        self._q, self._dtype = _QUANT[quant], _ACT[weight.dtype]
         self._call = B.lib().moe_rms_norm
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, want_y: bool = True,
@@ -124,8 +137,8 @@ class RMSNorm:
                 n = hidden // 32
                 scale = torch.empty_strided((shape[0], n), (n, 1), dtype=torch.uint8, device=dev)
                 sp = scale.data_ptr()
-        rc = self._call(x.data_ptr(), x.stride(0), rp, rs, self._w, self._dtype, shape[0], hidden, self.eps, ro, yp,
-                        self._q, self.fp8_scale, qp, sp, _raw_stream(dev.index))
+        rc = self._call(x.data_ptr(), x.stride(0), rp, rs, self.weight.data_ptr(), self._dtype, shape[0], hidden,
+                        self.eps, ro, yp, self._q, self.fp8_scale, qp, sp, _raw_stream(dev.index))
         if rc:
             B._check(rc)
         return NormResult(r, y, q, scale)
@@ -139,6 +152,8 @@ class KVBatch:
     each sequence with its new tokens.  rows: new tokens of all sequences;
     max_rows: at least the most of one sequence (rows if not given).  The
     tensors may be changed in place between calls."""
+
+    page_table, row_offsets, kv_len = (_bound(n) for n in ("page_table", "row_offsets", "kv_len"))
 
     def __init__(self, page_table: torch.Tensor, row_offsets: torch.Tensor, kv_len: torch.Tensor, rows: int,
                  max_rows: Optional[int] = None):
@@ -154,7 +169,7 @@ class KVBatch:
         max_rows = rows if max_rows is None else max_rows
         _require(rows >= 0 and 0 <= max_rows <= rows and (rows == 0 or max_rows > 0),
                  "rows %d and max_rows %d do not fit together" % (rows, max_rows))
-        self.page_table, self.row_offsets, self.kv_len = page_table, row_offsets, kv_len
+        self.__dict__.update(page_table=page_table, row_offsets=row_offsets, kv_len=kv_len)
         self.seqs, self.rows, self.max_rows = seqs, rows, max_rows
         self.c = B.MoeKvBatch(page_table.data_ptr(), row_offsets.data_ptr(), kv_len.data_ptr(), seqs,
                               page_table.shape[1], rows, max_rows)
@@ -168,6 +183,8 @@ class PagedKVCache:
     bf16, for an "f32" cache fp32.
 
     storage: (k, v, k_scale, v_scale) to use instead of new, zeroed pools."""
+
+    k, v, k_scale, v_scale = (_bound(n) for n in ("k", "v", "k_scale", "v_scale"))
 
     def __init__(self, kv_heads: int, head_dim: int, num_pages: int, page_size: int, dtype: str = "bf16",
                  device="cuda", storage=None):
@@ -192,7 +209,7 @@ class PagedKVCache:
                 _require(t is None or (tuple(t.shape) == want and t.dtype == kind and t.is_contiguous()
                                        and t.device == k.device),
                          "storage must be contiguous %s of %s on one device" % (list(want), kind))
-        self.k, self.v, self.k_scale, self.v_scale = k, v, ks, vs
+        self.__dict__.update(k=k, v=v, k_scale=ks, v_scale=vs)
         self.kv_heads, self.head_dim, self.num_pages, self.page_size = kv_heads, head_dim, num_pages, page_size
         self.dtype, self.device = dtype, _device(k)
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr() if mx else None,

@@ -435,3 +435,15 @@ def test_step_in_a_graph_follows_the_lengths(dtype):
         torch.cuda.synchronize()
         for t, u in zip(a, (res.residual, res.y, res.q, res.scale, out)):
             assert torch.equal(t, u), it
+
+
+def test_bound_tensors_are_not_replaced():
+    """Assigning another tensor would leave the old address in the C structs."""
+    p = R.Paged(gen(70), [1], [20], 16, 2, 64, "mxfp8")
+    cache, batch = p.device()
+    norm = block.RMSNorm(torch.ones(64, device="cuda"))
+    for obj, names in ((batch, ("page_table", "row_offsets", "kv_len")), (cache, ("k", "v", "k_scale", "v_scale")),
+                       (norm, ("weight",))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(obj, name, getattr(obj, name).clone())
