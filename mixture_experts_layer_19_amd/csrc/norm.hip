@@ -13,7 +13,8 @@
 // instructions cost 1.5% (8192 x 4096 bf16 with MX codes: 55.0 -> 55.8 us); the
 // rest of them runs under the loads.
 //
-// Bound by memory: a bf16 row with MX output moves 9.03 bytes an element.
+// Bound by memory: a bf16 row with MX output moves 9.03 bytes an element
+// (8192 x 4096: 59 us, 5.1 TB/s; a copy reaches 4.9).
 // One pass: a row stays in registers between the sum of squares and its use,
 // in one wave up to 2048 elements (no LDS, no barrier) and in a workgroup of
 // 256 up to 8192; longer rows, rows that are not 16-byte aligned and odd

@@ -447,3 +447,45 @@ def test_bound_tensors_are_not_replaced():
         for name in names:
             with pytest.raises(AttributeError):
                 setattr(obj, name, getattr(obj, name).clone())
+
+
+@pytest.mark.parametrize("dtype,hd,new,group", [("bf16", 64, 1, 2), ("mxfp8", 64, 1, 4), ("mxfp8", 128, 1, 8), ("f32", 128, 1, 1),
+                                                ("mxfp8", 128, 3, 8), ("bf16", 256, 1, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (600, 5)])
+def test_attention_cut_of_uneven_sequences(dtype, hd, new, group, window, sinks):
+    """More sequences than a wave has lanes and more tiles than runs; most are
+    short, some are empty or long, so that runs begin and end anywhere in a unit."""
+    n = 130
+    past = [(s * 37) % 211 if s % 9 else 900 + (s * 131) % 1500 for s in range(n)]
+    p = R.Paged(gen(80 + hd), [new * (s % 13 != 5) for s in range(n)], past, 16, 2, hd, dtype)
+    check_attention(p, 2 * group, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("past", [769, 1023, 1024, 1025, 1535])
+def test_attention_of_one_token_just_past_the_cut(dtype, past):
+    """Few units: about as many runs as positions, some without tiles."""
+    p = R.Paged(gen(90), [1], [past], 64, 1, 64, dtype)
+    check_attention(p, 3)
+
+
+def test_norm_codes_of_maxima_next_to_a_power_of_two():
+    """Rows whose largest y lies as close below or above 2^k as the inputs allow: the
+    scale is that of the 64-bit value, the codes are its nearest."""
+    g = gen(91)
+    x = torch.randn(512, 256, generator=g)
+    x[:, ::32] = x[:, ::32].abs() + 6.0                        # the largest of each block
+    s = x.to(torch.float32)
+    rms = (s.double().square().mean(1, keepdim=True) + 1e-5).sqrt()
+    w = torch.ones(256)
+    w[::32] = (4.0 / (s[0, ::32].double() / rms[0])).float()     # row 0: within a step of 4
+    near = s[0].clone()
+    rows = torch.stack([near * f for f in torch.linspace(0.999999, 1.000001, 512)])
+    res = block.RMSNorm(w.cuda(), quant="mxfp8")(rows.cuda())
+    rows64 = rows.double()
+    y = rows64 / (rows64.square().mean(1, keepdim=True) + float(torch.tensor(1e-5, dtype=torch.float32))).sqrt() * w.double()
+    top = y.unflatten(-1, (-1, 32)).abs().amax(-1)
+    # what the order of a 64-bit sum of 256 squares may move
+    sure = (top * (1 - 2.0 ** -44)).frexp()[1] == (top * (1 + 2.0 ** -44)).frexp()[1]
+    got = res.scale.cpu().int() - 127
+    assert ((got == top.frexp()[1] - 9) | ~sure).all() and sure.float().mean() > 0.9
