@@ -394,8 +394,7 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache *cache /* host */, const moe_k
  *
  * over the keys j <= pos(r); with window > 0 also j > pos(r) - window or
  * j < sinks.  A row that sees no key (or belongs to no sequence) gives zeros;
- * what masked slots hold, NaN included, does not reach a row whose whole
- * sequence masks them.  q: [rows][heads][head_dim], row and head strides in
+ * what slots hold that a row does not see, NaN included, does not reach it.  q: [rows][heads][head_dim], row and head strides in
  * elements, multiples of 16 bytes; out: [rows][heads][head_dim] contiguous.
  * Products of bf16 operands (MX-fp8 keys and values are exact in bf16) or
  * fp32 ones, accumulated in fp32; softmax statistics in fp32; with a bf16 or

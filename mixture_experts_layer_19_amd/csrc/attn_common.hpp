@@ -46,9 +46,9 @@ struct RowMask {
 };
 
 // Values that are not finite.  The second product multiplies every key of a
-// tile, also with the zero weights of rows that do not see it; so in tiles
-// that some rows see partly, elements that are not finite are zero in LDS and
-// are added afterwards, by add_not_finite, to the rows that do see them.
+// tile, also with the zero weights of rows that do not see it; so in tiles of
+// which some row does not see every key, elements that are not finite are zero in
+// LDS and are added afterwards, by add_not_finite, to the rows that do see them.
 //
 // Whether a 32-bit word of a pool holds one (MX: a NaN code).
 template <int F>

@@ -472,9 +472,10 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
         static_for<NKH>([&](auto kh) MOE_INLINE {
           if (!((there[kh] >> l16) & 1)) clear_v(vr[kh], vs[kh]);
         });
-      // keys that some rows of the tile see and others do not
+      // keys that exist and that not all rows see (of a single token too: behind its
+      // window, past its sinks)
       bool unsafe = false;
-      if (tok_b > tok_a && (k0 + C::keys > g.pos0 + tok_a + 1 || (a.window && k0 <= g.pos0 + tok_b - a.window)))
+      if (!inner)
         static_for<NKH>([&](auto kh) MOE_INLINE { unsafe = unsafe || not_finite(vr[kh], vs[kh]); });
       const bool fix = __ballot(unsafe) != 0;
       if (fix) store_v(std::true_type{});
