@@ -48,14 +48,16 @@ def _require(ok, what):
         raise ValueError(what)
 
 
-def _bound(name):
-    """An attribute whose address the C structs hold: its contents may change in
-    place, another tensor needs another object."""
-    def keep(self, value):
-        if value is not self.__dict__[name]:
-            raise AttributeError("%s is changed in place, not replaced" % name)
+class _Bound:
+    """Attributes (`_bound`) that the C structs copy or that lengths follow from: a
+    tensor's contents may change in place, another value needs another object."""
+    _bound = frozenset()
 
-    return property(lambda self: self.__dict__[name], keep)
+    def __setattr__(self, name, value):
+        if name in self._bound and value is not self.__dict__.get(name, value):
+            raise AttributeError("%s is not replaced; its contents may change in place, another one needs "
+                                 "another %s" % (name, type(self).__name__))
+        object.__setattr__(self, name, value)
 
 
 def _elsewhere(index, stream):
@@ -78,14 +80,14 @@ class NormResult(NamedTuple):
     scale: Optional[torch.Tensor]      # E8M0 bytes [rows, hidden / 32] (mxfp8 only)
 
 
-class RMSNorm:
+class RMSNorm(_Bound):
     """y = (x + residual) / sqrt(mean((x + residual)^2) + eps) * weight.
 
     quant: "none"; "mxfp8", E4M3 codes with an E8M0 scale byte per 32 elements;
     "fp8", E4M3 codes of y / fp8_scale.  The sum is held in fp32, the statistics
     and y in 64 bits; every output is rounded once from them."""
 
-    weight = _bound("weight")
+    _bound = frozenset(("weight", "quant", "hidden", "dtype", "device"))
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-5, quant: str = "none",
                  fp8_scale: float = 0.0):
@@ -96,7 +98,7 @@ class RMSNorm:
         _require(quant != "mxfp8" or weight.numel() % 32 == 0, "mxfp8 needs a hidden size in multiples of 32")
         _require(quant != "fp8" or 0.0 < fp8_scale < 3.0e38, "fp8 needs a positive fp8_scale")
         _require(eps >= 0.0, "eps must not be negative")
-        self.__dict__["weight"] = weight
+        self.weight = weight
         self.eps, self.quant, self.fp8_scale = float(eps), quant, float(fp8_scale)
         self.hidden, self.dtype = weight.numel(), weight.dtype
         self.device = _device(weight)
@@ -144,16 +146,17 @@ class RMSNorm:
         return NormResult(r, y, q, scale)
 
 
-class KVBatch:
+class KVBatch(_Bound):
     """New tokens of a batch of sequences and where their tokens lie.
 
     page_table [seqs, max_pages] int32 (entries that are no page hold nothing),
     row_offsets [seqs + 1] int32 ascending, kv_len [seqs] int32: the length of
     each sequence with its new tokens.  rows: new tokens of all sequences;
     max_rows: at least the most of one sequence (rows if not given).  The
-    tensors may be changed in place between calls."""
+    tensors may be changed in place between calls; other counts need another
+    batch."""
 
-    page_table, row_offsets, kv_len = (_bound(n) for n in ("page_table", "row_offsets", "kv_len"))
+    _bound = frozenset(("page_table", "row_offsets", "kv_len", "seqs", "rows", "max_rows", "device", "c"))
 
     def __init__(self, page_table: torch.Tensor, row_offsets: torch.Tensor, kv_len: torch.Tensor, rows: int,
                  max_rows: Optional[int] = None):
@@ -169,14 +172,14 @@ class KVBatch:
         max_rows = rows if max_rows is None else max_rows
         _require(rows >= 0 and 0 <= max_rows <= rows and (rows == 0 or max_rows > 0),
                  "rows %d and max_rows %d do not fit together" % (rows, max_rows))
-        self.__dict__.update(page_table=page_table, row_offsets=row_offsets, kv_len=kv_len)
+        self.page_table, self.row_offsets, self.kv_len = page_table, row_offsets, kv_len
         self.seqs, self.rows, self.max_rows = seqs, rows, max_rows
         self.c = B.MoeKvBatch(page_table.data_ptr(), row_offsets.data_ptr(), kv_len.data_ptr(), seqs,
                               page_table.shape[1], rows, max_rows)
         self._ref = ctypes.byref(self.c)
 
 
-class PagedKVCache:
+class PagedKVCache(_Bound):
     """Pools of pages [num_pages, kv_heads, page_size, head_dim] of keys and
     values: dtype "bf16", "f32" or "mxfp8" (uint8 E4M3 codes, and E8M0 scale
     bytes [num_pages, kv_heads, page_size, head_dim / 32]).  Activations are
@@ -184,7 +187,8 @@ class PagedKVCache:
 
     storage: (k, v, k_scale, v_scale) to use instead of new, zeroed pools."""
 
-    k, v, k_scale, v_scale = (_bound(n) for n in ("k", "v", "k_scale", "v_scale"))
+    _bound = frozenset(("k", "v", "k_scale", "v_scale", "kv_heads", "head_dim", "num_pages", "page_size", "dtype",
+                        "act_dtype", "device", "c"))
 
     def __init__(self, kv_heads: int, head_dim: int, num_pages: int, page_size: int, dtype: str = "bf16",
                  device="cuda", storage=None):
@@ -209,7 +213,7 @@ class PagedKVCache:
                 _require(t is None or (tuple(t.shape) == want and t.dtype == kind and t.is_contiguous()
                                        and t.device == k.device),
                          "storage must be contiguous %s of %s on one device" % (list(want), kind))
-        self.__dict__.update(k=k, v=v, k_scale=ks, v_scale=vs)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, ks, vs
         self.kv_heads, self.head_dim, self.num_pages, self.page_size = kv_heads, head_dim, num_pages, page_size
         self.dtype, self.device = dtype, _device(k)
         self.c = B.MoeKvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr() if mx else None,

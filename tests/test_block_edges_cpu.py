@@ -1,0 +1,57 @@
+"""The norm, the cache and the batch at their edges, as far as the host decides:
+the objects take tensors of the CPU here, and no call reaches the library."""
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_layer_19_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        from mixture_experts_layer_19_amd import build
+        build.build()
+    binding.lib()
+    return binding
+
+
+@pytest.fixture
+def block(B, monkeypatch):
+    from mixture_experts_layer_19_amd import block
+    monkeypatch.setattr(block, "_device", lambda t: t.device)
+    return block
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def objects(block):
+    batch = block.KVBatch(i32(3, 5), i32(4), i32(3), rows=10, max_rows=4)
+    cache = block.PagedKVCache(2, 64, 4, 16, dtype="mxfp8", device="cpu")
+    return batch, cache, block.RMSNorm(torch.ones(64), quant="mxfp8")
+
+
+def test_counts_stay_those_that_the_library_was_given(block):
+    """Assigning one would leave the old one in the C structs, which the kernels
+    count by, beside tensors of the new shape."""
+    batch, cache, norm = objects(block)
+    for obj, names in ((batch, ("seqs", "rows", "max_rows", "c")),
+                       (cache, ("kv_heads", "head_dim", "num_pages", "page_size", "c")), (norm, ("hidden",))):
+        for name in names:
+            was = getattr(obj, name)
+            for other in (2, 1000):
+                with pytest.raises(AttributeError):
+                    setattr(obj, name, other if was != other else other + 1)
+            assert getattr(obj, name) is was
+    for obj, name, other in ((cache, "dtype", "bf16"), (cache, "act_dtype", torch.float32),
+                             (cache, "device", torch.device("cuda", 0)), (batch, "device", torch.device("cuda", 0)),
+                             (norm, "quant", "none"), (norm, "dtype", torch.bfloat16),
+                             (norm, "device", torch.device("cuda", 0))):
+        with pytest.raises(AttributeError):
+            setattr(obj, name, other)
+    assert (batch.c.rows, batch.c.max_rows, batch.c.seqs) == (batch.rows, batch.max_rows, batch.seqs) == (10, 4, 3)
+    batch.kv_len += 1                                    # in place
+    assert batch.kv_len.tolist() == [1, 1, 1]
