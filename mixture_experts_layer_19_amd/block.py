@@ -123,21 +123,22 @@ class RMSNorm(_Bound):
         if other is not None:
             with other:
                 return self(x, residual, want_y=want_y)
-        # empty_like of rows that are contiguous inside is contiguous as a whole
-        like, r, y, q, scale = torch.empty_like, None, None, None, None
+        # (empty_like of overlapping rows need not be contiguous)
+        new, r, y, q, scale = torch.empty_strided, None, None, None, None
         rp = rs = ro = yp = qp = sp = 0
+        row = (hidden, 1)
         if residual is not None:
-            r = like(residual)
+            r = new(shape, row, dtype=self.dtype, device=dev)
             rp, rs, ro = residual.data_ptr(), residual.stride(0), r.data_ptr()
         if want_y:
-            y = like(x)
+            y = new(shape, row, dtype=self.dtype, device=dev)
             yp = y.data_ptr()
         if self._q != B.MOE_NO_QUANT:
-            q = like(x, dtype=torch.uint8)
+            q = new(shape, row, dtype=torch.uint8, device=dev)
             qp = q.data_ptr()
             if self._q == B.MOE_MXFP8:
                 n = hidden // 32
-                scale = torch.empty_strided((shape[0], n), (n, 1), dtype=torch.uint8, device=dev)
+                scale = new((shape[0], n), (n, 1), dtype=torch.uint8, device=dev)
                 sp = scale.data_ptr()
         rc = self._call(x.data_ptr(), x.stride(0), rp, rs, self.weight.data_ptr(), self._dtype, shape[0], hidden,
                         self.eps, ro, yp, self._q, self.fp8_scale, qp, sp, _raw_stream(dev.index))

@@ -78,3 +78,22 @@ def test_later_tokens_do_not_reach_row_tiles_inside_one_token(dtype, hd, page, g
     assert got[sees].isnan().all()
 
 
+# ----------------------------------------------------------------------------- views
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("quant", ["none", "mxfp8", "fp8"])
+@pytest.mark.parametrize("step", [1, 3, 0])
+def test_norm_of_overlapping_rows(dtype, quant, step):
+    """A sliding view (rows `step` elements apart) gives what its copy gives."""
+    w = (1 + 0.1 * torch.randn(64, generator=gen(1))).to(dtype).cuda()
+    a, b = (torch.randn(200, generator=gen(s)).to(dtype).cuda() for s in (2, 3))
+    x, r = (torch.as_strided(t, (37, 64), (step, 1)) for t in (a, b))
+    norm = block.RMSNorm(w, quant=quant, fp8_scale=0.03)
+    for args in ((x, r), (x,), (x.contiguous(), r), (x, r.contiguous())):
+        got, want = norm(*args), norm(*(t.contiguous() for t in args))
+        for g, v in zip(got, want):
+            assert (g is None) == (v is None)
+            assert g is None or (g.is_contiguous() and torch.equal(g, v))
+
+
