@@ -332,7 +332,8 @@ MOE_API moe_status moe_layer_forward_noalloc(moe_ctx *ctx, const moe_desc *desc 
  * [rows][hidden] contiguous and may be the inputs if those are, too.
  * q_dtype: MOE_NO_QUANT; MOE_MXFP8 (q E4M3 [rows][hidden], q_scale E8M0
  * [rows][hidden/32], the rule of moe_mx_quantize; hidden a multiple of 32);
- * MOE_FP8 (E4M3 of y / fp8_scale, the rule of moe_fp8_quantize).  A NaN
+ * MOE_FP8 (E4M3 of y / fp8_scale in 64 bits, round to nearest even,
+ * saturating: moe_fp8_quantize without its rounding to fp32).  A NaN
  * becomes the NaN code and an infinity saturates.  residual_out is NULL
  * exactly where residual is; y may be NULL with an 8-bit output.  Any
  * hidden >= 1; x, residual, weight, y and residual_out need only their

@@ -84,8 +84,8 @@ class RMSNorm(_Bound):
     """y = (x + residual) / sqrt(mean((x + residual)^2) + eps) * weight.
 
     quant: "none"; "mxfp8", E4M3 codes with an E8M0 scale byte per 32 elements;
-    "fp8", E4M3 codes of y / fp8_scale.  The sum is held in fp32, the statistics
-    and y in 64 bits; every output is rounded once from them."""
+    "fp8", E4M3 codes of y / fp8_scale.  The sum is held in fp32, the
+    statistics, y and y / fp8_scale in 64 bits; every output is rounded once from them."""
 
     _bound = frozenset(("weight", "quant", "hidden", "dtype", "device"))
 

@@ -5,13 +5,13 @@
 //   residual_out = round(s), y_out = round(y)
 //   q = E4M3 codes of y: under one E8M0 scale per 32 (MX) or of y / fp8_scale
 //
-// The sum is held in fp32 (exact for nearly all bf16 operands), the statistic
-// and y in 64 bits, and every output is rounded once from them: y goes to bf16
-// and to the codes by way of fp32 rounded to odd, which keeps what lies below
-// and above a tie or a power of two apart (y in fp32 moved the scale, and with
-// it 32 codes, of a block whose maximum lay next to a power of two).  The 64-bit
-// instructions cost 1.5% (8192 x 4096 bf16 with MX codes: 55.0 -> 55.8 us); the
-// rest of them runs under the loads.
+// The sum is held in fp32 (exact for nearly all bf16 operands), the statistic,
+// y and y / fp8_scale in 64 bits, and every output is rounded once from them: y
+// goes to bf16 and to the codes by way of fp32 rounded to odd, which keeps what
+// lies below and above a tie or a power of two apart (y in fp32 moved the scale,
+// and with it 32 codes, of a block whose maximum lay next to a power of two).  The
+// 64-bit instructions cost 1.5% (8192 x 4096 bf16 with MX codes: 55.0 -> 55.8 us);
+// the rest of them runs under the loads.
 //
 // Bound by memory: a bf16 row with MX output moves 9.03 bytes an element
 // (8192 x 4096: 59 us, 5.1 TB/s; a copy reaches 4.9).
@@ -82,15 +82,19 @@ __device__ __forceinline__ float round_f32(double d) {
   u -= fabs((double)n) > fabs(d) ? 1u : 0u;
   return __uint_as_float(u | ((double)n != d ? 1u : 0u));
 }
-// y of 8 elements: `out` to be stored as the row's type, `code` for the codes.
-template <bool BF16>
-__device__ __forceinline__ void norm8(const float (&v)[8], double rs, const float (&w)[8], float (&out)[8],
-                                      float (&code)[8]) {
+// y of 8 elements: `out` to be stored as the row's type, `code` for the codes (FP8:
+// y by the scale, in 64 bits as y is; the scale's inverse, 8192 x 4096 57.5 us,
+// adds a rounding of 2^-53 to the quotient's, 67.8).
+template <bool BF16, int Q>
+__device__ __forceinline__ void norm8(const NormArgs &a, const float (&v)[8], double rs, const float (&w)[8],
+                                      float (&out)[8], float (&code)[8]) {
+  const double rq = Q == FMT_FP8 ? 1.0 / (double)a.fp8_scale : 1.0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const double d = (double)v[j] * rs * (double)w[j];
-    code[j] = round_f32<true>(d);
-    out[j] = BF16 ? code[j] : round_f32<false>(d);
+    const float odd = round_f32<true>(d);
+    code[j] = Q == FMT_FP8 ? round_f32<true>(d * rq) : odd;
+    out[j] = BF16 ? odd : round_f32<false>(d);
   }
 }
 
@@ -114,11 +118,7 @@ __device__ __forceinline__ void store_codes(const NormArgs &a, long long i, int 
       if ((threadIdx.x & 3) == 0) a.q_scale[i >> 5] = (uint8_t)sb;
     }
   } else if constexpr (Q == FMT_FP8) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = y[j] / a.fp8_scale;
-    const uint2 w = make_uint2(e4m3_pack4(v[0], v[1], v[2], v[3]),
-                               e4m3_pack4(v[4], v[5], v[6], v[7]));
+    const uint2 w = make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3]), e4m3_pack4(y[4], y[5], y[6], y[7]));
     if (whole) {
       *(uint2 *)(a.q + i) = w;
     } else {
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       if (a.residual_out) store8<BF16>(a.residual_out, at, v[i]);
       float w[8];
       load8<BF16>(a.weight, 8 * c, w);
-      norm8<BF16>(v[i], rs, w, y, code);
+      norm8<BF16, Q>(a, v[i], rs, w, y, code);
       if (a.y) store8<BF16>(a.y, at, y);
     } else {
 #pragma unroll
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void norm_loop_kernel(NormArgs a) {
         load_n<BF16>(a.weight, 8 * c, n, w);
         if (a.residual_out) store_n<BF16>(a.residual_out, at, n, v);
       }
-      norm8<BF16>(v, rs, w, y, code);
+      norm8<BF16, Q>(a, v, rs, w, y, code);
       if (a.y) {
         if constexpr (VEC) store8<BF16>(a.y, at, y);
         else store_n<BF16>(a.y, at, n, y);

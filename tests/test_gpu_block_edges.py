@@ -97,3 +97,45 @@ def test_norm_of_overlapping_rows(dtype, quant, step):
             assert g is None or (g.is_contiguous() and torch.equal(g, v))
 
 
+# ----------------------------------------------------------------------------- roundings
+
+
+@pytest.mark.parametrize("hidden", [256, 4096, 4097, 9000])
+@pytest.mark.parametrize("scale", [0.01, 0.37, 3.0])
+def test_norm_fp8_codes_next_to_ties(hidden, scale):
+    """y / fp8_scale as close to the middle of two codes as fp32 weights allow: the
+    codes are those of the 64-bit quotient."""
+    g = gen(hidden)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    eps = float(torch.tensor(1e-5, dtype=torch.float32))
+    x = torch.randn(hidden, generator=g).abs() + 0.1
+    rms = (x.double().square().mean() + eps).sqrt()
+    # the middle of the values with mantissas m and m + 1 of eight
+    m = torch.randint(0, 8, (hidden,), generator=g).double()
+    tie = torch.ldexp(1 + (m + 0.5) / 8, torch.randint(-5, 7, (hidden,), generator=g))
+    w = (tie * scale * rms / x.double()).float()
+    want = x.double() / rms * w.double() / scale
+    sure = (want / tie - 1).abs() > 2.0 ** -44              # what the order of a 64-bit sum may move
+    assert sure.float().mean() > 0.9
+    low, high = torch.ldexp(1 + m / 8, tie.frexp()[1] - 1), torch.ldexp(1 + (m + 1) / 8, tie.frexp()[1] - 1)
+    got = block.RMSNorm(w.cuda(), eps=1e-5, quant="fp8", fp8_scale=scale)(x.cuda().view(1, -1)).q[0]
+    got = got.cpu().view(torch.float8_e4m3fn).double()
+    assert torch.equal(got[sure], torch.where(want < tie, low, high)[sure])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,hidden", [(3, 64), (5, 1000), (4, 4096), (3, 8191), (2, 20000)])
+def test_norm_is_rounded_once(dtype, rows, hidden):
+    """residual and y lie within half a step of the fp32 sum and of y in 64 bits."""
+    g = gen(hidden)
+    x, r = (torch.randn(rows, hidden, generator=g).to(dtype) for _ in "xr")
+    w = torch.randn(hidden, generator=g).to(dtype)
+    res = block.RMSNorm(w.cuda(), eps=1e-5)(x.cuda(), r.cuda())
+    s = x.float() + r.float()
+    assert torch.equal(res.residual.cpu(), s.to(dtype))
+    eps = float(torch.tensor(1e-5, dtype=torch.float32))
+    _, y = R.norm_ref(s, None, w, eps)
+    # 2^-44: the order of a 64-bit sum, its root, the quotient and two products
+    assert ((res.y.cpu().double() - y).abs() <= (R.half_step(dtype) + 2.0 ** -44) * y.abs()).all()
+
+
