@@ -77,8 +77,9 @@ moe_status attn_args(const moe_kv_cache *cache, const moe_kv_batch *batch, int h
   if ((long long)a->c.rows * heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   a->heads = heads;
   a->group = heads / cache->kv_heads;
-  // a window that covers the table hides nothing
-  if ((long long)window >= ((long long)a->c.max_pages << a->c.page_shift)) window = 0;
+  // a window or sinks that cover the table hide nothing
+  const long long tokens = (long long)a->c.max_pages << a->c.page_shift;
+  if (window >= tokens || sinks >= tokens) window = 0;
   a->window = window;
   a->sinks = window ? sinks : 0;
   return MOE_OK;

@@ -55,3 +55,27 @@ def test_counts_stay_those_that_the_library_was_given(block):
     assert (batch.c.rows, batch.c.max_rows, batch.c.seqs) == (batch.rows, batch.max_rows, batch.seqs) == (10, 4, 3)
     batch.kv_len += 1                                    # in place
     assert batch.kv_len.tolist() == [1, 1, 1]
+
+
+P = 1 << 20          # a pointer that is aligned and never read
+
+
+def cache_of(B, **kw):
+    return B.MoeKvCache(**dict(dict(k=P, v=P, k_scale=P, v_scale=P, num_pages=10, page_size=16, kv_heads=2, head_dim=128,
+                                    dtype=B.MOE_MXFP8), **kw))
+
+
+def batch_of(B, **kw):
+    return B.MoeKvBatch(**dict(dict(page_table=P, row_offsets=P, kv_len=P, seqs=3, max_pages=200, rows=6, max_rows=2),
+                               **kw))
+
+
+def test_sinks_that_cover_the_table_hide_nothing(B):
+    """Their number does not overflow: the cut, and its workspace, are those without a window."""
+    for max_pages in (200, 100000):
+        for rows, max_rows in ((6, 2), (600, 300)):
+            c, b = cache_of(B), batch_of(B, max_pages=max_pages, rows=rows, max_rows=max_rows)
+            whole = B.moe_attention_workspace_bytes(c, b, 4, 0, 0)
+            assert whole > 0
+            for sinks in (16 * max_pages, 2 ** 31 - 128, 2 ** 31 - 1):
+                assert B.moe_attention_workspace_bytes(c, b, 4, 100, sinks) == whole

@@ -139,3 +139,21 @@ def test_norm_is_rounded_once(dtype, rows, hidden):
     assert ((res.y.cpu().double() - y).abs() <= (R.half_step(dtype) + 2.0 ** -44) * y.abs()).all()
 
 
+# ----------------------------------------------------------------------------- small pages, many sinks
+
+
+def check(p, heads, window=0, sinks=0):
+    q = torch.randn(p.rows, heads, p.hd, generator=gen(6)).to(p.act)
+    cache, batch = p.device()
+    got = cache.attention(batch, q.cuda(), window=window, sinks=sinks).cpu().double()
+    want, bound = R.attention_ref(p, q, p.hd ** -0.5, window, sinks)
+    assert ((got - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("new", [[1], [40]])
+@pytest.mark.parametrize("sinks", [2500, 2 ** 31 - 1, 2 ** 40])
+def test_sinks_that_cover_the_context(dtype, new, sinks):
+    check(R.Paged(gen(sinks % 1000), new, [2300], 16, 1, 64, dtype), 2, 50, sinks)
+
+
