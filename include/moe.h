@@ -400,8 +400,11 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache *cache /* host */, const moe_k
  * Products of bf16 operands (MX-fp8 keys and values are exact in bf16) or
  * fp32 ones, accumulated in fp32; softmax statistics in fp32; with a bf16 or
  * MX-fp8 cache the softmax weights are rounded to bf16 before they multiply
- * the values.  ws: moe_attention_workspace_bytes() bytes (0: none needed, or
- * invalid arguments), its contents need not outlive the call's kernels. */
+ * the values.  Batches of more units (sequences x KV heads x their tiles of
+ * rows) than one launch or 32-bit counts hold, some millions, return
+ * MOE_ERR_UNSUPPORTED.  ws: moe_attention_workspace_bytes() bytes (0: none
+ * needed, or invalid arguments), its contents need not outlive the call's
+ * kernels. */
 MOE_API size_t moe_attention_workspace_bytes(const moe_kv_cache *cache /* host */,
                                      const moe_kv_batch *batch /* host */, int32_t heads,
                                      int32_t window, int32_t sinks);

@@ -664,7 +664,20 @@ struct Launch {
     }
     return tiles <= 6;
   }
-  static bool fits(const AttnArgs &a) { return most(a.c, a.group) >= 0; }
+  // Units, and what the join's launch holds of them: rows of a unit, at most, and
+  // how many of them a workgroup takes.
+  static long long all_units(const KvArgs &c, int group) { return (long long)c.seqs * c.kv_heads * units(c, group); }
+  static int unit_rows(const AttnArgs &a) {
+    const long long rows = (long long)a.c.max_rows * a.group;
+    return (int)(rows < C::rows ? rows : C::rows);
+  }
+  static int per(const AttnArgs &a) { return all_units(a.c, a.group) < 256 ? 1 : 1024 / HD; }
+  static long long join_groups(const AttnArgs &a) {
+    return all_units(a.c, a.group) * ((unit_rows(a) + per(a) - 1) / per(a));
+  }
+  static bool fits(const AttnArgs &a) {
+    return most(a.c, a.group) >= 0 && (whole(a) ? all_units(a.c, a.group) : join_groups(a)) <= max_groups(256);
+  }
   static size_t ws(const AttnArgs &a) {
     return whole(a) ? 0 : (size_t)grid(a.c, a.group) * 2 * C::rows * (HD + 2) * sizeof(float);
   }
@@ -678,19 +691,15 @@ struct Launch {
   }
   static hipError_t run(const AttnArgs &args, hipStream_t s) {
     AttnArgs a = args;
-    const int u = units(a.c, a.group), all = a.c.seqs * a.c.kv_heads * u;
+    const int u = units(a.c, a.group);
     if (whole(a)) {
-      a.grid = all;
+      a.grid = (int)all_units(a.c, a.group);
       return rows<true>(a, u, s);
     }
     a.grid = grid(a.c, a.group);
     const hipError_t err = rows<false>(a, u, s);
     if (err != hipSuccess) return err;
-    // rows of a unit, at most
-    const long long rows = (long long)a.c.max_rows * a.group;
-    const int unit_rows = (int)(rows < C::rows ? rows : C::rows);
-    const int per = all < 256 ? 1 : 1024 / HD;
-    attn_join_kernel<F, HD, RT, NKH><<<(unsigned)(all * ((unit_rows + per - 1) / per)), 256, 0, s>>>(a, unit_rows, u, per);
+    attn_join_kernel<F, HD, RT, NKH><<<(unsigned)join_groups(a), 256, 0, s>>>(a, unit_rows(a), u, per(a));
     return hipGetLastError();
   }
 };

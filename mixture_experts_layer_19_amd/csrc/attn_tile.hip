@@ -580,7 +580,7 @@ struct TileLaunch {
   }
   static bool fits(const AttnArgs &a) {
     const long long u = units(a) * a.c.kv_heads;
-    return u * splits(a) <= INT32_MAX && u * (C::rows / (1024 / HD)) <= INT32_MAX;
+    return u * splits(a) <= max_groups(C::threads) && u * (C::rows / (1024 / HD)) <= max_groups(256);
   }
   static size_t ws(const AttnArgs &a) {
     const int s = splits(a);

@@ -7,6 +7,10 @@
 
 namespace moe {
 
+// Workgroups of `threads` that one launch holds: past 2^32 threads it would run
+// part of them, without an error.
+constexpr long long max_groups(int threads) { return (1ll << 32) / threads - 1; }
+
 // Row strides are in elements.  Null pointers: residual / residual_out (no
 // residual), y (8-bit output only), q and q_scale (no 8-bit output).
 struct NormArgs {

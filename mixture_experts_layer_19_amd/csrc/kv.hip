@@ -22,6 +22,7 @@ struct KvIo {
   long long k_row, k_head, v_row, v_head;
   int piece_shift;             // log2 of the 16-byte pieces of a head
   uint32_t per_row;            // 2^32 / (2 kv_heads), rounded up
+  int first;                   // first row of this launch
 };
 
 // Place of each of the workgroup's rows in the pool, head 0 (kNoRow: none).
@@ -68,7 +69,7 @@ constexpr int kBatch = 4;      // pieces of a thread in flight
 template <int F, int R>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
   __shared__ uint32_t place[R];
-  const int row0 = blockIdx.x * R, rows = min(R, c.rows - row0);
+  const int row0 = io.first + blockIdx.x * R, rows = min(R, c.rows - row0);
   const int pieces = (rows * 2 * c.kv_heads) << io.piece_shift;
   uint4 u[kBatch];
   auto load = [&](int i0) MOE_INLINE {
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
 template <int F, int R>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs c, KvIo io) {
   __shared__ uint32_t place[R];
-  const int row0 = blockIdx.x * R, rows = min(R, c.rows - row0);
+  const int row0 = io.first + blockIdx.x * R, rows = min(R, c.rows - row0);
   const int pieces = (rows * 2 * c.kv_heads) << io.piece_shift;
   find_rows<R>(c, row0, place);
   __syncthreads();
@@ -177,24 +178,38 @@ int rows_of_group(int rows) { return (rows + 3) / 4 <= 2048 ? 4 : 8; }
 KvIo io_args(const KvArgs &c, void *k, void *v, long long k_row, long long k_head, long long v_row, long long v_head) {
   const int pieces = c.head_dim / (c.fmt == FMT_F32 ? 4 : 8);
   const uint64_t d = 2ull * c.kv_heads;
-  return {k, v, k_row, k_head, v_row, v_head, __builtin_ctz(pieces), (uint32_t)(((1ull << 32) + d - 1) / d)};
+  return {k, v, k_row, k_head, v_row, v_head, __builtin_ctz(pieces), (uint32_t)(((1ull << 32) + d - 1) / d), 0};
+}
+
+// f(R, workgroups, io) for the rows of each launch.
+template <typename Fn>
+hipError_t each_launch(const KvArgs &c, KvIo io, Fn &&f) {
+  constexpr int kRows = 1 << 25;
+  static_assert(kRows / 4 <= max_groups(256), "rows of a launch");
+  const int r = rows_of_group(c.rows);
+  for (long long row0 = 0; row0 < c.rows; row0 += kRows) {
+    io.first = (int)row0;
+    const long long n = c.rows - row0 < kRows ? c.rows - row0 : kRows;
+    f(r, (unsigned)((n + r - 1) / r), io);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 template <int F>
-hipError_t write(const KvArgs &c, const KvIo &io, hipStream_t s) {
-  const int r = rows_of_group(c.rows);
-  const unsigned grid = (unsigned)((c.rows + r - 1) / r);
-  if (r == 4) kv_write_kernel<F, 4><<<grid, 256, 0, s>>>(c, io);
-  else kv_write_kernel<F, 8><<<grid, 256, 0, s>>>(c, io);
-  return hipGetLastError();
+hipError_t write(const KvArgs &c, const KvIo &all, hipStream_t s) {
+  return each_launch(c, all, [&](int r, unsigned grid, const KvIo &io) {
+    if (r == 4) kv_write_kernel<F, 4><<<grid, 256, 0, s>>>(c, io);
+    else kv_write_kernel<F, 8><<<grid, 256, 0, s>>>(c, io);
+  });
 }
 template <int F>
-hipError_t read(const KvArgs &c, const KvIo &io, hipStream_t s) {
-  const int r = rows_of_group(c.rows);
-  const unsigned grid = (unsigned)((c.rows + r - 1) / r);
-  if (r == 4) kv_read_kernel<F, 4><<<grid, 256, 0, s>>>(c, io);
-  else kv_read_kernel<F, 8><<<grid, 256, 0, s>>>(c, io);
-  return hipGetLastError();
+hipError_t read(const KvArgs &c, const KvIo &all, hipStream_t s) {
+  return each_launch(c, all, [&](int r, unsigned grid, const KvIo &io) {
+    if (r == 4) kv_read_kernel<F, 4><<<grid, 256, 0, s>>>(c, io);
+    else kv_read_kernel<F, 8><<<grid, 256, 0, s>>>(c, io);
+  });
 }
 }  // namespace
 

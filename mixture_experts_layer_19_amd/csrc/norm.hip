@@ -197,7 +197,7 @@ template <bool BF16, int Q, bool VEC>
 __global__ __launch_bounds__(256) void norm_loop_kernel(NormArgs a) {
   __shared__ double red[4];
   const int row = blockIdx.x, tid = threadIdx.x;
-  const int nvec = (a.hidden + 7) / 8;
+  const int nvec = a.hidden / 8 + (a.hidden % 8 != 0);
   auto load = [&](int c, float (&v)[8]) {
     const int n = min(8, a.hidden - 8 * c);
     float r[8];
@@ -268,18 +268,35 @@ void launch(const NormArgs &a, hipStream_t s) {
 }
 }  // namespace
 
-hipError_t launch_rms_norm(const NormArgs &a, int is_bf16, int q_fmt, hipStream_t s) {
-  if (a.rows <= 0) return hipSuccess;
-  if (is_bf16) {
-    if (q_fmt == FMT_MX8) launch<true, FMT_MX8>(a, s);
-    else if (q_fmt == FMT_FP8) launch<true, FMT_FP8>(a, s);
-    else launch<true, -1>(a, s);
-  } else {
-    if (q_fmt == FMT_MX8) launch<false, FMT_MX8>(a, s);
-    else if (q_fmt == FMT_FP8) launch<false, FMT_FP8>(a, s);
-    else launch<false, -1>(a, s);
+hipError_t launch_rms_norm(const NormArgs &all, int is_bf16, int q_fmt, hipStream_t s) {
+  constexpr int kRows = 1 << 23;                 // of a launch: up to a workgroup each
+  static_assert(kRows <= max_groups(256), "rows of a launch");
+  const int e = is_bf16 ? 2 : 4;
+  for (long long r0 = 0; r0 < all.rows; r0 += kRows) {
+    NormArgs a = all;
+    auto skip = [&](auto *&p, long long bytes) {
+      if (p) p = (std::remove_reference_t<decltype(p)>)((const uint8_t *)p + r0 * bytes);
+    };
+    skip(a.x, all.x_stride * e);
+    skip(a.residual, all.residual_stride * e);
+    skip(a.residual_out, (long long)all.hidden * e);
+    skip(a.y, (long long)all.hidden * e);
+    skip(a.q, all.hidden);
+    skip(a.q_scale, all.hidden / 32);
+    a.rows = (int)(all.rows - r0 < kRows ? all.rows - r0 : kRows);
+    if (is_bf16) {
+      if (q_fmt == FMT_MX8) launch<true, FMT_MX8>(a, s);
+      else if (q_fmt == FMT_FP8) launch<true, FMT_FP8>(a, s);
+      else launch<true, -1>(a, s);
+    } else {
+      if (q_fmt == FMT_MX8) launch<false, FMT_MX8>(a, s);
+      else if (q_fmt == FMT_FP8) launch<false, FMT_FP8>(a, s);
+      else launch<false, -1>(a, s);
+    }
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace moe

@@ -79,3 +79,16 @@ def test_sinks_that_cover_the_table_hide_nothing(B):
             assert whole > 0
             for sinks in (16 * max_pages, 2 ** 31 - 128, 2 ** 31 - 1):
                 assert B.moe_attention_workspace_bytes(c, b, 4, 100, sinks) == whole
+
+
+@pytest.mark.parametrize("c,b,heads", [
+    # a workgroup a unit; pieces of cut units to join; tiles of 256 rows
+    (dict(kv_heads=8), dict(seqs=1 << 21, rows=1 << 21, max_rows=1, max_pages=2), 8),
+    (dict(kv_heads=8), dict(seqs=1 << 21, rows=1 << 21, max_rows=1, max_pages=100), 8),
+    (dict(kv_heads=8, head_dim=256), dict(seqs=1 << 19, rows=1 << 20, max_rows=2, max_pages=100), 64),
+    (dict(kv_heads=8), dict(seqs=1 << 20, rows=1 << 21, max_rows=2, max_pages=2), 512)])
+def test_attention_refuses_more_units_than_a_launch_holds(B, c, b, heads):
+    """A launch of 2^32 threads and more would run part of them."""
+    with pytest.raises(B.MoeError) as ei:
+        B.moe_attention(cache_of(B, **c), batch_of(B, **b), P, 512 * heads, 512, heads, 0.1, 0, 0, P, P, 1 << 50)
+    assert ei.value.status == B.MOE_ERR_UNSUPPORTED

@@ -157,3 +157,45 @@ def test_sinks_that_cover_the_context(dtype, new, sinks):
     check(R.Paged(gen(sinks % 1000), new, [2300], 16, 1, 64, dtype), 2, 50, sinks)
 
 
+# ----------------------------------------------------------------------------- sizes
+
+
+def test_norm_of_more_rows_than_one_launch():
+    """A workgroup takes one row of an odd length; a launch holds fewer than 2^24 of 256 threads."""
+    rows, hidden = (1 << 24) + 3, 7
+    x = torch.randn(rows, hidden, device="cuda").to(torch.bfloat16)
+    w = torch.randn(hidden, device="cuda").to(torch.bfloat16)
+    res = block.RMSNorm(w, eps=1e-5, quant="fp8", fp8_scale=0.5)(x, x)
+    for a in range(0, rows, 1 << 22):
+        s = 2 * x[a:a + (1 << 22)].float()
+        assert torch.equal(res.residual[a:a + (1 << 22)], s.to(torch.bfloat16))
+        y = s.double() / torch.sqrt(s.double().square().mean(1, keepdim=True) + 1e-5) * w.double()
+        far = (res.y[a:a + (1 << 22)].double() - y).abs()
+        # eps is 1e-5 rounded to fp32
+        assert (far <= (R.BF16_HALF + 2.0 ** -24) * y.abs()).all()
+        q = res.q[a:a + (1 << 22)].view(torch.float8_e4m3fn).double() * 0.5
+        assert ((q - y).abs() <= (R.MX_HALF + 2.0 ** -24) * y.abs() + 2.0 ** -11).all()
+
+
+def test_cache_calls_of_more_rows_than_one_launch():
+    """2^27 + 5 new tokens (strides of zero: one row stands for all) of which only the
+    last page is there."""
+    rows, page, hd = (1 << 27) + 5, 65536, 64
+    table = torch.full((1, (rows + page - 1) // page), -1, dtype=torch.int32)
+    table[0, -1] = 1
+    cache = block.PagedKVCache(1, hd, 2, page, dtype="bf16")
+    offsets, kv_len = (torch.tensor(t, dtype=torch.int32).cuda() for t in ([0, rows], [rows]))
+    batch = block.KVBatch(table.cuda(), offsets, kv_len, rows=rows)
+    k, v = (torch.randn(1, 1, hd, generator=gen(s)).to(torch.bfloat16).cuda() for s in (1, 2))
+    cache.write(batch, k.expand(rows, 1, hd), v.expand(rows, 1, hd))
+    torch.cuda.synchronize()
+    for pool, x in ((cache.k, k), (cache.v, v)):
+        assert torch.equal(pool[1, 0, :5], x[0].expand(5, hd))
+        assert (pool[1, 0, 5:] == 0).all() and (pool[0] == 0).all()
+    rk, rv = cache.read(batch)
+    for got, x in ((rk, k), (rv, v)):
+        assert torch.equal(got[-5:], x.expand(5, 1, hd))
+        for a in range(0, rows - 5, 1 << 24):
+            assert not got[a:min(a + (1 << 24), rows - 5)].view(torch.int64).any()
+
+
