@@ -459,7 +459,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
         for (int kh = 0; kh < NKH; ++kh)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(sc[rt][kh][i], a.scale, -mx[rt]));
+            const float p = __builtin_amdgcn_exp2f(mul_sub(sc[rt][kh][i], a.scale, mx[rt]));
             sc[rt][kh][i] = p;
             part += p;
           }

@@ -361,6 +361,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     static_for<AHEAD>([&](auto n) MOE_INLINE { read(half, n); });
     __builtin_amdgcn_sched_barrier(0);
   };
+  const int far_exp = far_exponent(a.scale);
   auto step = [&](auto half, int t, unsigned long long have, bool is_plain, bool v_plain, f32x16 &cur, f32x16 &next,
                   Weights &w, const Weights &last) MOE_INLINE {
     if (!is_plain) {
@@ -379,7 +380,8 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
     // spread over the slots, and their sum and rounding follow one slot behind.
     constexpr int FIRST = 2, SPAN = SLOTS - FIRST - 1;
     __builtin_amdgcn_sched_barrier(0);
-    float top = -INFINITY, now = 0.0f, alpha = 0.0f, part[2] = {0.0f, 0.0f};
+    bool far = false;
+    float top = -INFINITY, now = 0.0f, alpha = 0.0f, mul = a.scale, part[2] = {0.0f, 0.0f};
     static_for<SLOTS>([&](auto n) MOE_INLINE {
       if constexpr (n == 0)
 #pragma unroll
@@ -390,18 +392,25 @@ __global__ __launch_bounds__(64 * NW, OCC) void attn_tile_kernel(AttnArgs a, int
       if constexpr (n == 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, cur[i]);
+        far = __ballot(__builtin_amdgcn_frexp_expf(top) > far_exp) != 0;
       }
       if constexpr (n == 1) {
         top = max_half(top) * a.scale;             // the scale is positive
         // the reference moves only when a score passes it by 2^8
         now = top > mx + 8.0f ? top : mx;
         alpha = __builtin_amdgcn_exp2f(mx - now);
+        if (__builtin_expect(far, 0)) {
+          asm volatile("");                        // a branch, not selects
+          mul = 1.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) cur[i] *= a.scale;
+        }
       }
       // elements whose exponentials are due in slot n: [due(n), due(n + 1))
       auto due = [](int m) constexpr { return m <= FIRST ? 0 : m >= FIRST + SPAN ? 16 : 16 * (m - FIRST) / SPAN; };
       constexpr int e0 = due(n), e1 = due(n + 1), d0 = due(n - 1);
 #pragma unroll
-      for (int i = e0; i < e1; ++i) cur[i] = __builtin_amdgcn_exp2f(fmaf(cur[i], a.scale, -now));
+      for (int i = e0; i < e1; ++i) cur[i] = __builtin_amdgcn_exp2f(fmaf(cur[i], mul, -now));
 #pragma unroll
       for (int i = d0; i < e0; ++i) {
         part[i % 2] += cur[i];

@@ -12,7 +12,20 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(2))) int i32x2;
 
-constexpr float kNegBig = -1e30f;     // running maximum before any key: finite, below every score
+constexpr float kNegBig = -3.402823466e38f;   // running maximum before any key: finite, below every score
+// The weight of a score s is exp2(s * scale - reference).  As one fused operation
+// that does not round the product as the reference was rounded, which scales all
+// weights of a row alike, by up to 2^(|reference| / 2^24): 2^16 at 2^28, but past
+// fp32 from 2^31 on.  So the product is rounded first (x s - r in two steps): where
+// memory is the bound, always; where the vector units are, only in half tiles with a
+// score whose exponent (frexp) is above far_exponent, a product of 2^27 or more.
+// There (chunks of 640-1408 tokens) the test costs 0.6% (861 -> 866 us), one of the
+// scaled maximum 2%, products rounded everywhere 5%.
+__device__ __forceinline__ float mul_sub(float x, float s, float r) {
+#pragma clang fp contract(off)
+  return x * s - r;
+}
+__device__ __forceinline__ int far_exponent(float scale) { return 28 + 126 - (int)(__float_as_uint(scale) >> 23); }
 
 // v, its magnitude limited to 448; a NaN stays one.
 __device__ __forceinline__ float e4m3_clamp(float v) {

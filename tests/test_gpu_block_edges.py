@@ -199,3 +199,54 @@ def test_cache_calls_of_more_rows_than_one_launch():
             assert not got[a:min(a + (1 << 24), rows - 5)].view(torch.int64).any()
 
 
+# ----------------------------------------------------------------------------- far scores
+
+
+def far_scores(dtype, new, page, group, hd, power, sign):
+    """A batch whose rows all score sign * 1.6015625 * 2^power * (1, or 2 at every third
+    position): its q, and the positions whose score is the largest."""
+    p = R.Paged(gen(hd + power), new, [70 + 300 * (s % 2) for s in range(len(new))], page, 1, hd, dtype)
+    q = torch.randn(p.rows, group, hd, generator=gen(7)).to(p.act)
+    q[..., 1:] = 0.0
+    q[..., 0] = 1.6015625 * 2.0 ** (power - power // 2)
+    k, scales = p.pools[0]
+    best = []
+    for s, t in enumerate(p.total):
+        two = [j % 3 == 1 for j in range(t)]
+        for j in range(t):
+            at = p.table[s, j // page], slice(None), j % page
+            if dtype == "mxfp8":                         # codes of 1 and 2
+                k[at] = 0
+                k[at + (0,)] = (0x40 if two[j] else 0x38) | (0x80 if sign < 0 else 0)
+                scales[at] = 127 + power // 2
+            else:
+                k[at] = 0.0
+                k[at + (0,)] = sign * (2.0 if two[j] else 1.0) * 2.0 ** (power // 2)
+        best.append([b == (sign > 0) for b in two])
+    return p, q, best
+
+
+@pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("power", [12, 24, 31, 32, 34, 40, 60, 100, 110, 126])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("new,page,group,hd", [([1, 1], 16, 4, 64), ([3], 16, 8, 128), ([50, 3], 16, 4, 64),
+                                               ([70], 64, 8, 128), ([40], 32, 2, 256)])
+def test_scores_far_from_zero(dtype, power, sign, new, page, group, hd):
+    """The keys with the largest score share the weight, however large the scores are
+    (all of them finite in fp32)."""
+    p, q, best = far_scores(dtype, new, page, group, hd, power, sign)
+    cache, batch = p.device()
+    got = cache.attention(batch, q.cuda(), scale=0.73).cpu().double()
+    first = 0
+    for s, n in enumerate(new):
+        v = p.context(s, 1)[0]
+        for i in range(n):
+            pos = p.total[s] - n + i
+            j = torch.tensor(best[s][:pos + 1]).nonzero()[:, 0]
+            want, a = v[j].mean(0), v[j].abs().mean(0)
+            # the weights are equal and sum to one: as in _block.attention_ref without a score's error
+            rel = 2.0 ** -21 + (len(j) + 64) * R.F32_HALF + (R.BF16_HALF if dtype != "f32" else 0.0)
+            assert ((got[first + i] - want).abs() <= R.half_step(p.act) * want.abs() + rel * a).all(), (s, i)
+        first += n
+
+
