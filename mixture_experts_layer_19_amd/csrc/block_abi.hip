@@ -168,10 +168,12 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   a.q = q;
   a.q_row = q_row;
   a.q_head = q_head;
-  // the kernels take maxima of unscaled scores, so the scale's sign goes into q;
-  // a zero scale becomes one that no product of finite scores notices
+  // the kernels take maxima of unscaled scores, so the scale's sign goes into q; zero
+  // times a masked score's -inf would be NaN, so a zero scale becomes the smallest
+  // that is not (2^-149 times any score is below 2^-21), and an infinite product
+  // with log2(e) the largest (whose scores, but zero, are as far apart)
   a.q_sign = scale < 0.0f ? (a.c.fmt == FMT_F32 ? 0x80000000u : 0x80008000u) : 0u;
-  a.scale = fmaxf(fabsf(scale) * 1.44269504088896340736f, 1.2e-38f);
+  a.scale = fminf(fmaxf(fabsf(scale) * 1.44269504088896340736f, 0x1p-149f), 0x1.fffffep127f);
   a.out = out;
   a.part = (float *)ws;
   a.grid = 0;

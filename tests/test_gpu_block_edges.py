@@ -250,3 +250,24 @@ def test_scores_far_from_zero(dtype, power, sign, new, page, group, hd):
         first += n
 
 
+@pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("new", [[1, 2], [70]])
+def test_scales_at_the_ends_of_fp32(dtype, new):
+    """A scale of zero or of a subnormal hides the scores, whatever they are; the largest
+    scale leaves scores of zero at zero."""
+    p, q, _ = far_scores(dtype, new, 16, 4, 64, 124, 1)
+    cache, batch = p.device()
+    for scale, factor in ((0.0, 1.0), (1e-44, 1.0), (-1e-44, 1.0), (3.4e38, 0.0), (-3.4e38, 0.0)):
+        got = cache.attention(batch, q.cuda() * factor, scale=scale).cpu().double()
+        first = 0
+        for s, n in enumerate(new):
+            v = p.context(s, 1)[0]
+            for i in range(n):
+                seen = v[:p.total[s] - n + i + 1]
+                want, a = seen.mean(0), seen.abs().mean(0)
+                # scores of up to 2^126 * 1e-44: 2^-20, either way
+                rel = 2.0 ** -18 + (len(seen) + 64) * R.F32_HALF + (R.BF16_HALF if dtype != "f32" else 0.0)
+                assert ((got[first + i] - want).abs() <= R.half_step(p.act) * want.abs() + rel * a).all()
+            first += n
+
+
