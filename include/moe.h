@@ -375,12 +375,12 @@ typedef struct moe_kv_batch {
 } moe_kv_batch;
 
 /* Write the new tokens' keys and values ([rows][kv_heads][head_dim]; row and
- * head strides in elements, multiples of 16 bytes) into their pages,
- * quantised to MX-fp8 where the cache is (the rule of moe_mx_quantize over
- * head_dim; a NaN becomes the NaN code).  Rows of no sequence or page are
- * dropped.  moe_kv_read is the way back: k, v [rows][kv_heads][head_dim]
- * contiguous, dequantised and rounded once; zeros for rows of no sequence or
- * page. */
+ * head strides in elements, multiples of 16 bytes unless there is only one row
+ * or head) into their pages, quantised to MX-fp8 where the cache is (the rule of
+ * moe_mx_quantize over head_dim; a NaN becomes the NaN code).  Rows of no
+ * sequence or page are dropped.  moe_kv_read is the way back: k, v
+ * [rows][kv_heads][head_dim] contiguous, dequantised and rounded once; zeros
+ * for rows of no sequence or page. */
 MOE_API moe_status moe_kv_write(const moe_kv_cache *cache /* host */, const moe_kv_batch *batch /* host */,
                         const void *k, int64_t k_row, int64_t k_head, const void *v,
                         int64_t v_row, int64_t v_head, void *stream);
@@ -396,7 +396,7 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache *cache /* host */, const moe_k
  * over the keys j <= pos(r); with window > 0 also j > pos(r) - window or
  * j < sinks.  A row that sees no key (or belongs to no sequence) gives zeros;
  * what slots hold that a row does not see, NaN included, does not reach it.  q: [rows][heads][head_dim], row and head strides in
- * elements, multiples of 16 bytes; out: [rows][heads][head_dim] contiguous.
+ * elements, as above; out: [rows][heads][head_dim] contiguous.
  * Products of bf16 operands (MX-fp8 keys and values are exact in bf16) or
  * fp32 ones, accumulated in fp32; softmax statistics in fp32; with a bf16 or
  * MX-fp8 cache the softmax weights are rounded to bf16 before they multiply

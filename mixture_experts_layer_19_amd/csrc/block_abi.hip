@@ -63,10 +63,10 @@ moe_status kv_args(const moe_kv_cache *c, const moe_kv_batch *b, KvArgs *o) {
 }
 
 // Strides in elements of a [rows][heads][head_dim] operand of the cache's
-// activation type: whole 16-byte pieces.
-bool strides_ok(const KvArgs &c, int64_t row, int64_t head) {
+// activation type: whole 16-byte pieces, along axes of more than one.
+bool strides_ok(const KvArgs &c, int heads, int64_t row, int64_t head) {
   const int e = c.fmt == FMT_F32 ? 4 : 8;
-  return row % e == 0 && head % e == 0;
+  return (c.rows == 1 || row % e == 0) && (heads == 1 || head % e == 0);
 }
 
 moe_status attn_args(const moe_kv_cache *cache, const moe_kv_batch *batch, int heads, int window,
@@ -130,8 +130,8 @@ moe_status moe_kv_write(const moe_kv_cache *cache, const moe_kv_batch *batch, co
   KvArgs c;
   moe_status st = kv_args(cache, batch, &c);
   if (st != MOE_OK || c.rows == 0) return st;
-  if (!k || !v || !al(k, 16) || !al(v, 16) || !strides_ok(c, k_row, k_head) ||
-      !strides_ok(c, v_row, v_head))
+  if (!k || !v || !al(k, 16) || !al(v, 16) || !strides_ok(c, c.kv_heads, k_row, k_head) ||
+      !strides_ok(c, c.kv_heads, v_row, v_head))
     return MOE_ERR_INVALID_ARG;
   return done(launch_kv_write(c, k, v, k_row, k_head, v_row, v_head, (hipStream_t)stream));
 }
@@ -160,7 +160,7 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   if (st != MOE_OK) return st;
   if (!(scale - scale == 0.0f)) return MOE_ERR_INVALID_ARG;      // infinite or NaN
   if (a.c.rows == 0) return MOE_OK;
-  if (!q || !out || !al(q, 16) || !al(out, 16) || !al(ws, 16) || !strides_ok(a.c, q_row, q_head))
+  if (!q || !out || !al(q, 16) || !al(out, 16) || !al(ws, 16) || !strides_ok(a.c, heads, q_row, q_head))
     return MOE_ERR_INVALID_ARG;
   const size_t need = workspace(a);
   if (!(few_rows(a) ? attn_rows_fits(a) : attn_tile_fits(a))) return MOE_ERR_UNSUPPORTED;

@@ -271,3 +271,22 @@ def test_scales_at_the_ends_of_fp32(dtype, new):
             first += n
 
 
+@pytest.mark.parametrize("dtype", CACHES)
+def test_strides_that_no_element_uses(dtype):
+    """The stride of an axis of one row or one head does not matter."""
+    p = R.Paged(gen(3), [1], [40], 16, 1, 64, dtype)
+    cache, batch = p.device()
+    q = torch.randn(1, 2, 64, generator=gen(4)).to(p.act).cuda()
+    kv = torch.randn(1, 1, 64, generator=gen(5)).to(p.act).cuda()
+    odd = torch.as_strided(kv, (1, 1, 64), (77, 33, 1))
+    want = cache.attention(batch, q)
+    assert torch.equal(cache.attention(batch, torch.as_strided(q, (1, 2, 64), (131, 64, 1))), want)
+    one = torch.as_strided(q, (1, 1, 64), (131, 7, 1))
+    assert torch.equal(cache.attention(batch, one), cache.attention(batch, q[:, :1].contiguous()))
+    cache.write(batch, odd, odd)
+    k, v = cache.read(batch)
+    cache.write(batch, kv, kv)
+    for got, again in zip((k, v), cache.read(batch)):
+        assert torch.equal(got, again)
+
+
