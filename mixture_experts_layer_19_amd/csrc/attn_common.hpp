@@ -13,8 +13,19 @@
 // query heads that share keys fill a matrix tile together.
 #pragma once
 #include "block_common.hpp"
+#include "once_per_device.hpp"
 
 namespace moe {
+
+// Allow `bytes` of dynamic LDS to a kernel on the current device; `once`: of that kernel.
+inline hipError_t allow_lds(OncePerDevice &once, const void *kernel, int bytes) {
+  int device = 0;
+  const hipError_t err = hipGetDevice(&device);
+  if (err != hipSuccess) return err;
+  return (hipError_t)once(device, [&] {
+    return (int)hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
 
 // Key tiles of BK keys that tokens [i0, i1] of a sequence visit: the tiles
 // that hold sinks, then those of the window.

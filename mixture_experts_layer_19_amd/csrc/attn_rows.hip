@@ -683,9 +683,9 @@ struct Launch {
   }
   template <bool WHOLE>
   static hipError_t rows(const AttnArgs &a, int u, hipStream_t s) {
-    static const hipError_t once = hipFuncSetAttribute((const void *)attn_rows_kernel<F, HD, RT, NKH, WHOLE>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
-    if (once != hipSuccess) return once;
+    static OncePerDevice once;
+    const hipError_t err = allow_lds(once, (const void *)attn_rows_kernel<F, HD, RT, NKH, WHOLE>, C::lds);
+    if (err != hipSuccess) return err;
     attn_rows_kernel<F, HD, RT, NKH, WHOLE><<<a.grid, 256, C::lds, s>>>(a, u);
     return hipGetLastError();
   }

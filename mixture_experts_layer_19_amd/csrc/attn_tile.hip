@@ -598,9 +598,9 @@ struct TileLaunch {
   static hipError_t run(const AttnArgs &a, hipStream_t st) {
     const int s = splits(a);
     const long long u = units(a) * a.c.kv_heads, grid = u * s;
-    static const hipError_t once = hipFuncSetAttribute((const void *)attn_tile_kernel<F, HD, NW, OCC>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::lds);
-    if (once != hipSuccess) return once;
+    static OncePerDevice once;
+    const hipError_t err = allow_lds(once, (const void *)attn_tile_kernel<F, HD, NW, OCC>, C::lds);
+    if (err != hipSuccess) return err;
     attn_tile_kernel<F, HD, NW, OCC><<<(unsigned)grid, C::threads, C::lds, st>>>(a, s);
     if (s > 1)
       attn_tile_join_kernel<F, HD, NW><<<(unsigned)(u * (C::rows / (1024 / HD))), 256, 0, st>>>(a, s);

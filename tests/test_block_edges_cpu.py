@@ -92,3 +92,43 @@ def test_attention_refuses_more_units_than_a_launch_holds(B, c, b, heads):
     with pytest.raises(B.MoeError) as ei:
         B.moe_attention(cache_of(B, **c), batch_of(B, **b), P, 512 * heads, 512, heads, 0.1, 0, 0, P, P, 1 << 50)
     assert ei.value.status == B.MOE_ERR_UNSUPPORTED
+
+
+ONCE = r"""
+#include "once_per_device.hpp"
+#include <assert.h>
+#include <thread>
+#include <vector>
+int main() {
+  moe::OncePerDevice once;
+  int calls[80] = {0};
+  auto call = [&](int d, int result) { return once(d, [&] { ++calls[d]; return result; }); };
+  assert(call(0, 0) == 0 && call(0, 0) == 0 && calls[0] == 1);      // set once
+  assert(call(1, 0) == 0 && calls[1] == 1 && calls[0] == 1);        // another device: of its own
+  assert(call(2, 7) == 7 && call(2, 7) == 7 && calls[2] == 2);      // a failure is not kept
+  assert(call(2, 0) == 0 && call(2, 7) == 0 && calls[2] == 3);
+  assert(call(63, 0) == 0 && call(63, 1) == 0 && calls[63] == 1);
+  assert(call(70, 0) == 0 && call(70, 0) == 0 && calls[70] == 2);   // past the mask: every time
+  moe::OncePerDevice other;
+  std::atomic<int> n{0};
+  std::vector<std::thread> t;
+  for (int i = 0; i < 16; ++i)
+    t.emplace_back([&, i] { for (int k = 0; k < 1000; ++k) other(i % 4, [&] { ++n; return 0; }); });
+  for (auto &x : t) x.join();
+  assert(n >= 4 && n <= 16);
+  return 0;
+}
+"""
+
+
+def test_a_kernels_setting_is_made_on_every_device(tmp_path):
+    """The limit of dynamic LDS belongs to a kernel on one device."""
+    import subprocess
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mixture_experts_layer_19_amd", "csrc")
+    src = tmp_path / "once.cpp"
+    src.write_text(ONCE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", csrc, str(src), "-o", str(tmp_path / "once")], check=True)
+    subprocess.run([str(tmp_path / "once")], check=True, timeout=60)
+    for name in ("attn_rows.hip", "attn_tile.hip"):
+        text = open(os.path.join(csrc, name)).read()
+        assert "hipFuncSetAttribute" not in text and "allow_lds(once" in text
