@@ -64,6 +64,7 @@ def _elsewhere(index, stream):
     """A context in which the current device and stream are the call's, or None
     if they are already."""
     if stream is not None:
+        _require(stream.device_index == index, "the stream is of another device than the tensors")
         return torch.cuda.stream(stream)
     return None if _current_device() == index else torch.cuda.device(index)
 

@@ -1,6 +1,7 @@
 """The norm, the cache and the batch at their edges, as far as the host decides:
 the objects take tensors of the CPU here, and no call reaches the library."""
 import os
+import types
 
 import pytest
 
@@ -132,3 +133,16 @@ def test_a_kernels_setting_is_made_on_every_device(tmp_path):
     for name in ("attn_rows.hip", "attn_tile.hip"):
         text = open(os.path.join(csrc, name)).read()
         assert "hipFuncSetAttribute" not in text and "allow_lds(once" in text
+
+
+def test_streams_of_another_device_are_refused(block):
+    """The call would have run on that device's current stream, beside the one given."""
+    batch, cache, norm = objects(block)
+    for index in (1, 7):
+        other = types.SimpleNamespace(device_index=index, device=torch.device("cuda", index))
+        for call in (lambda: norm(torch.ones(2, 64), stream=other),
+                     lambda: cache.read(batch, stream=other),
+                     lambda: cache.write(batch, *(torch.zeros(10, 2, 64, dtype=torch.bfloat16),) * 2, stream=other),
+                     lambda: cache.attention(batch, torch.zeros(10, 4, 64, dtype=torch.bfloat16), stream=other)):
+            with pytest.raises(ValueError, match="another device"):
+                call()
