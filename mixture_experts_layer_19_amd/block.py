@@ -34,6 +34,7 @@ _CACHE = {"bf16": (B.MOE_BF16, torch.bfloat16, torch.bfloat16),
           "f32": (B.MOE_F32, torch.float32, torch.float32),
           # OCP MX-fp8: E4M3 codes and one E8M0 scale byte per 32 elements of head_dim
           "mxfp8": (B.MOE_MXFP8, torch.uint8, torch.bfloat16)}
+_INT32 = 0x7FFFFFFF   # the library counts rows, pages and positions in 32 bits; ctypes would cut a larger one
 _QUANT = {"none": B.MOE_NO_QUANT, "mxfp8": B.MOE_MXFP8, "fp8": B.MOE_FP8}
 # Small calls are bound by the host: the checks build no message unless they
 # fail, the library's functions are called with plain integers, and the stream
@@ -92,8 +93,8 @@ class RMSNorm(_Bound):
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-5, quant: str = "none",
                  fp8_scale: float = 0.0):
-        _require(weight.dim() == 1 and weight.is_contiguous() and weight.numel() > 0,
-                 "weight must be a contiguous vector")
+        _require(weight.dim() == 1 and weight.is_contiguous() and 0 < weight.numel() <= _INT32,
+                 "weight must be a contiguous vector of fewer than 2^31 elements")
         _require(weight.dtype in _ACT, "weight must be float32 or bfloat16, got %s" % weight.dtype)
         _require(quant in _QUANT, "quant must be one of %s, got %r" % (sorted(_QUANT), quant))
         _require(quant != "mxfp8" or weight.numel() % 32 == 0, "mxfp8 needs a hidden size in multiples of 32")
@@ -118,6 +119,8 @@ class RMSNorm(_Bound):
                                  % (hidden, self.dtype, dev, list(t.shape), t.dtype, t.device))
             if t.stride(1) != 1 and hidden != 1:
                 raise ValueError("rows must be contiguous")
+        if shape[0] > _INT32:
+            raise ValueError("%d rows are more than 2^31 - 1" % shape[0])
         if not want_y and self._q == B.MOE_NO_QUANT:
             raise ValueError("without y there is no output")
         other = _elsewhere(dev.index, stream)
@@ -172,6 +175,7 @@ class KVBatch(_Bound):
             _require(t.dtype == torch.int32 and t.is_contiguous() and t.device == self.device,
                      "page_table, row_offsets and kv_len must be contiguous int32 on one device")
         max_rows = rows if max_rows is None else max_rows
+        _require(max(rows, seqs, page_table.shape[1]) <= _INT32, "rows, sequences and pages of one must be below 2^31")
         _require(rows >= 0 and 0 <= max_rows <= rows and (rows == 0 or max_rows > 0),
                  "rows %d and max_rows %d do not fit together" % (rows, max_rows))
         self.page_table, self.row_offsets, self.kv_len = page_table, row_offsets, kv_len
@@ -196,6 +200,7 @@ class PagedKVCache(_Bound):
                  device="cuda", storage=None):
         _require(dtype in _CACHE, "dtype must be one of %s, got %r" % (sorted(_CACHE), dtype))
         _require(kv_heads > 0 and num_pages > 0 and page_size > 0, "a cache needs heads, pages and slots")
+        _require(max(kv_heads, num_pages) <= _INT32, "heads and pages must be below 2^31")
         _require(page_size & (page_size - 1) == 0 and page_size <= 65536,
                  "page_size must be a power of two up to 65536, got %d" % page_size)
         _require(head_dim in (64, 128, 256), "head_dim must be 64, 128 or 256, got %d" % head_dim)
@@ -283,7 +288,7 @@ class PagedKVCache(_Bound):
             self._check(batch, out, heads, "out")
             _require(out.is_contiguous(), "out must be contiguous")
         # the library counts positions in 32 bits: a larger window hides nothing either
-        window, sinks = min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF)
+        window, sinks = min(window, _INT32), min(sinks, _INT32)
         other = _elsewhere(self.device.index, stream)
         if other is not None:
             with other:

@@ -146,3 +146,18 @@ def test_streams_of_another_device_are_refused(block):
                      lambda: cache.attention(batch, torch.zeros(10, 4, 64, dtype=torch.bfloat16), stream=other)):
             with pytest.raises(ValueError, match="another device"):
                 call()
+
+
+def test_counts_past_32_bits_are_refused(block):
+    """Passing one on would cut it to its low 32 bits: 2^32 + 5 rows would be 5."""
+    _, cache, norm = objects(block)
+    with pytest.raises(ValueError, match="2.31"):
+        norm(torch.ones(1, 64).expand(2 ** 32 + 5, 64))
+    with pytest.raises(ValueError, match="2.31"):
+        norm(torch.ones(1, 64).expand(2 ** 31, 64))
+    for rows in (2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError, match="2.31"):
+            block.KVBatch(i32(3, 5), i32(4), i32(3), rows=rows)
+    for kw in (dict(kv_heads=2 ** 32 + 1), dict(num_pages=2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="2.31"):
+            block.PagedKVCache(**dict(dict(kv_heads=1, head_dim=64, num_pages=1, page_size=1, device="meta"), **kw))
