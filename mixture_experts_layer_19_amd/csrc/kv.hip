@@ -10,9 +10,9 @@
 // Bound by memory: a bf16 token's head of 128 is 256 bytes on one side and
 // 132 (MX) or 256 on the other.  A workgroup takes R rows, a thread 16 bytes of
 // activations at a time, four pieces in flight; when writing, the first four
-// are on their way while the rows' places are looked up.  Measured, MX-fp8, 8
-// heads of 128: 8900 tokens written 15.5 us (3.6 TB/s), 37000 read 48.7 us
-// (4.6 TB/s).
+// are on their way while the rows' places are looked up.  Measured, 8 heads of
+// 128: 8900 tokens written into MX-fp8 15.6 us (3.6 TB/s), bf16 13.5 (5.4), fp32
+// 29.5 (5.0); 37000 tokens of MX-fp8 read 48.7 us (4.6 TB/s).
 #include "block_common.hpp"
 
 namespace moe {
@@ -71,16 +71,17 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
   __shared__ uint32_t place[R];
   const int row0 = io.first + blockIdx.x * R, rows = min(R, c.rows - row0);
   const int pieces = (rows * 2 * c.kv_heads) << io.piece_shift;
-  uint4 u[kBatch];
+  // Four loads without a condition (past the end the last piece again), into vectors:
+  // as structs behind a `break` the bf16 and fp32 ones went through LDS one by one
+  // (8900 tokens 24.5 and 41.0 us).
+  i32x4 u[kBatch];
   auto load = [&](int i0) MOE_INLINE {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + 256 * b + threadIdx.x;
-      if (i >= pieces) break;
-      const Piece<F> p(c, io, i);
+      const Piece<F> p(c, io, min(i0 + 256 * b + (int)threadIdx.x, pieces - 1));
       const long long at = (long long)(row0 + p.row) * (p.side ? io.v_row : io.k_row) +
                            p.h * (p.side ? io.v_head : io.k_head) + p.d;
-      u[b] = *(const uint4 *)((const uint8_t *)(p.side ? io.v : io.k) + at * (16 / Piece<F>::E));
+      u[b] = *(const i32x4 *)((const uint8_t *)(p.side ? io.v : io.k) + at * (16 / Piece<F>::E));
     }
   };
   load(0);
@@ -91,21 +92,20 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs c, KvIo io) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int i = i0 + 256 * b + threadIdx.x;
-      if (i >= pieces) break;
+      if (i >= pieces) continue;
       const Piece<F> p(c, io, i);
       const uint32_t at = place[p.row];
       if (at == kNoRow) continue;
       const long long dst = (long long)(at + ((uint32_t)p.h << c.page_shift)) * c.head_dim + p.d;
       uint8_t *pool = p.side ? c.v : c.k;
       if constexpr (F != FMT_MX8) {
-        *(uint4 *)(pool + dst * (16 / Piece<F>::E)) = u[b];
+        *(i32x4 *)(pool + dst * (16 / Piece<F>::E)) = u[b];
       } else {
-        const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
         float v[8], am = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[2 * j] = __uint_as_float(w[j] << 16);
-          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          v[2 * j] = __uint_as_float((uint32_t)u[b][j] << 16);
+          v[2 * j + 1] = __uint_as_float((uint32_t)u[b][j] & 0xFFFF0000u);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(v[j]));

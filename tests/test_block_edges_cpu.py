@@ -161,3 +161,21 @@ def test_counts_past_32_bits_are_refused(block):
     for kw in (dict(kv_heads=2 ** 32 + 1), dict(num_pages=2 ** 32 + 1)):
         with pytest.raises(ValueError, match="2.31"):
             block.PagedKVCache(**dict(dict(kv_heads=1, head_dim=64, num_pages=1, page_size=1, device="meta"), **kw))
+
+
+def test_cache_kernels_keep_their_pieces_in_registers(tmp_path):
+    """The pieces in flight are in registers: beside the rows' places (4 bytes each of 4
+    or 8 rows) the compiler gives the kernels neither LDS nor scratch memory."""
+    import re
+    import subprocess
+    from mixture_experts_layer_19_amd import build
+    cmd = [build._hipcc(), "--offload-arch=" + build.ARCH, "-O3", "-std=c++17", "-fPIC", "-Xclang", "-target-feature",
+           "-Xclang", "-packed-fp32-ops", "-I", os.path.join(build.ROOT, "include"), "--cuda-device-only",
+           "-Rpass-analysis=kernel-resource-usage", "-c", os.path.join(build.CSRC, "kv.hip"), "-o", str(tmp_path / "kv.o")]
+    text = subprocess.run(cmd, check=True, capture_output=True, text=True, timeout=300).stderr
+    names = re.findall(r"Function Name: (\S+)", text)
+    lds = [int(n) for n in re.findall(r"LDS Size \[bytes/block\]: (\d+)", text)]
+    scratch = [int(n) for n in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", text)]
+    assert len(names) == len(lds) == len(scratch) == 12
+    for name, n, s in zip(names, lds, scratch):
+        assert n <= 32 and s == 0, name
