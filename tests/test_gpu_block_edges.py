@@ -290,3 +290,12 @@ def test_strides_that_no_element_uses(dtype):
         assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("dtype", CACHES)
+@pytest.mark.parametrize("page", [1, 2, 4])
+@pytest.mark.parametrize("new,past,kvh,group,hd", [([1, 1], [300, 17], 2, 4, 64), ([1], [1100], 1, 8, 128),
+                                                   ([37, 5], [20, 1000], 1, 4, 64), ([33], [90], 2, 2, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 3)])
+def test_pages_of_fewer_than_eight_tokens(dtype, page, new, past, kvh, group, hd, window, sinks):
+    check(R.Paged(gen(page + hd), new, past, page, kvh, hd, dtype), kvh * group, window, sinks)
+
+
