@@ -19,8 +19,9 @@
 // instruction reads; V goes through the wave's own LDS, read transposed.
 //
 // Measured, 64 heads over 8 KV heads of 128: 64 sequences of up to 8100 MX-fp8
-// keys 114 us (5.1 TB/s), 8 of up to 131071 bf16 keys 413 us (5.9 TB/s), one of
-// 937 bf16 keys 11 us, of which the join 4.
+// keys 114 us (5.1 TB/s), bf16 204 (5.5), 8 of up to 131071 bf16 keys 412 us (5.9
+// TB/s), one of 937 bf16 keys 12 us, of which the join 4; fp32, up to 4000 keys,
+// 209 us (5.4 TB/s); 32 sequences of 4 tokens over MX-fp8 74 us (4.0).
 #include "attn_common.hpp"
 
 namespace moe {
@@ -475,7 +476,7 @@ __global__ __launch_bounds__(256, (RowsCfg<F, HD, RT, NKH>::occupancy)) void att
       // keys that exist and that not all rows see (of a single token too: behind its
       // window, past its sinks)
       bool unsafe = false;
-      if (!inner)
+      if (min(k0 + C::keys, g.len) > all_hi || (k0 < all_lo && k0 + C::keys > a.sinks))
         static_for<NKH>([&](auto kh) MOE_INLINE { unsafe = unsafe || not_finite(vr[kh], vs[kh]); });
       const bool fix = __ballot(unsafe) != 0;
       if (fix) store_v(std::true_type{});
