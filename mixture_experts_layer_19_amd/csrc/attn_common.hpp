@@ -8,6 +8,12 @@
 // maxima, sums and the output accumulate in fp32; the softmax runs on powers
 // of two (scale * log2(e) is folded into the scores).
 //
+// With a bf16 or MX cache the weights are rounded to bf16 for the second product,
+// whose matrix instructions take bf16 (fp32 ones run at a tenth of the rate); their
+// sum is taken before that, in fp32.  Half a step of bf16 a key, independent from key
+// to key: the results lie 0.0023 of their size from 64 bits, 0.0017 with fp32
+// weights, of which the output's own rounding to bf16 is nearly all.
+//
 // The rows of one sequence and KV head are the pairs (token, query head of
 // the group), token-major: row m is token m / group, head m % group.  So the
 // query heads that share keys fill a matrix tile together.

@@ -25,9 +25,9 @@
 // workspace in the order of their keys (attn_tile_join_kernel).
 //
 // Measured, 64 heads over 8 KV heads of 128: 4 chunks of 640-1408 tokens over up
-// to 7501 bf16 keys before them 871 us (988 TFLOP/s; the matrix cores work 49% of
+// to 7501 bf16 keys before them 866 us (994 TFLOP/s; the matrix cores work 49% of
 // the time, the vector units 45%), 4001 tokens under a window of 1024 over
-// MX-fp8 210 us (642).
+// MX-fp8 209 us (645).  The same chunks at head_dim 64 545 us (789), 256 2440 (705).
 #include "attn_common.hpp"
 
 namespace moe {
@@ -611,7 +611,8 @@ struct TileLaunch {
 // Waves a workgroup and workgroups of four waves a CU: as many as the registers
 // hold.  head_dim 64 at three (bf16 8 registers short, kept in memory) against
 // two: chunks of 640-1408 tokens over up to 7501 keys 562 and 598 us, a window
-// of 1024 129 and 147; one of eight waves: 606.
+// of 1024 129 and 147; one of eight waves: 606.  head_dim 256 fills a wave's
+// registers (bf16 keeps 36 bytes a lane in memory).
 template <typename Fn>
 auto pick_tile(const KvArgs &c, Fn &&f) {
   if (c.fmt == FMT_F32) return c.head_dim == 64 ? f(TileLaunch<FMT_F32, 64, 4, 2>{}) : f(TileLaunch<FMT_F32, 128, 4, 1>{});

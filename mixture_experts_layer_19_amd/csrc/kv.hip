@@ -11,8 +11,9 @@
 // 132 (MX) or 256 on the other.  A workgroup takes R rows, a thread 16 bytes of
 // activations at a time, four pieces in flight; when writing, the first four
 // are on their way while the rows' places are looked up.  Measured, 8 heads of
-// 128: 8900 tokens written into MX-fp8 15.6 us (3.6 TB/s), bf16 13.5 (5.4), fp32
-// 29.5 (5.0); 37000 tokens of MX-fp8 read 48.7 us (4.6 TB/s).
+// 128: 8900 tokens written into MX-fp8 15.0 us (3.7 TB/s), bf16 13.8 (5.3), fp32
+// 28.4 (5.1); 37000 tokens read from MX-fp8 48.7 us (4.6 TB/s), bf16 50.6 (5.8),
+// fp32 115 (5.1).
 #include "block_common.hpp"
 
 namespace moe {

@@ -14,11 +14,12 @@
 // the rest of them runs under the loads.
 //
 // Bound by memory: a bf16 row with MX output moves 9.03 bytes an element
-// (8192 x 4096: 59 us, 5.1 TB/s; a copy reaches 4.9).
+// (8192 x 4096: 60 us, 5.0 TB/s; a copy reaches 4.9).
 // One pass: a row stays in registers between the sum of squares and its use,
 // in one wave up to 2048 elements (no LDS, no barrier) and in a workgroup of
 // 256 up to 8192; longer rows, rows that are not 16-byte aligned and odd
-// lengths are read a second time (norm_loop_kernel).
+// lengths are read a second time (norm_loop_kernel: 2048 x 16384 bf16 with MX codes
+// 90 us, 3.4 TB/s; 8192 x 4095, element by element, 236 us, 1.3 TB/s).
 #include "block_common.hpp"
 
 namespace moe {
