@@ -349,7 +349,8 @@ MOE_API moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *res
  * dtype MOE_BF16 or MOE_F32: elements; MOE_MXFP8: E4M3 codes, with E8M0
  * scale bytes [num_pages][kv_heads][page_size][head_dim/32].  page_size: a
  * power of two up to 65536; kv_heads up to 1024; head_dim 64, 128 or 256;
- * num_pages * kv_heads * page_size below 2^32 - 1.  Activations are bf16 (fp32 for a MOE_F32 cache). */
+ * num_pages * kv_heads * page_size below 2^32 - 1.  Activations are bf16 (fp32
+ * for a MOE_F32 cache). */
 typedef struct moe_kv_cache {
   void *k, *v;
   uint8_t *k_scale, *v_scale;    /* MOE_MXFP8 only */

@@ -299,3 +299,19 @@ def test_pages_of_fewer_than_eight_tokens(dtype, page, new, past, kvh, group, hd
     check(R.Paged(gen(page + hd), new, past, page, kvh, hd, dtype), kvh * group, window, sinks)
 
 
+# ----------------------------------------------------------------------------- in place
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,hidden", [(5, 512), (3, 2048), (3, 4096), (2, 8192), (3, 1023), (2, 9000), (2, 20008)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_norm_in_place(dtype, rows, hidden, swap):
+    """residual_out and y in the memory of the residual and of x, either way round."""
+    x, r = (torch.randn(rows, hidden, generator=gen(s + hidden)).to(dtype).cuda() for s in (1, 2))
+    w = torch.randn(hidden, generator=gen(3)).to(dtype).cuda()
+    want = block.RMSNorm(w, quant="fp8", fp8_scale=0.1)(x, r)
+    q = torch.empty(rows, hidden, dtype=torch.uint8, device="cuda")
+    ro, y = (x, r) if swap else (r, x)
+    B.moe_rms_norm(x, hidden, r, hidden, w, B.MOE_BF16 if dtype == torch.bfloat16 else B.MOE_F32, rows, hidden, 1e-5,
+                   ro, y, B.MOE_FP8, 0.1, q, None)
+    assert torch.equal(ro, want.residual) and torch.equal(y, want.y) and torch.equal(q, want.q)
