@@ -313,7 +313,9 @@ MOE_API moe_status moe_layer_forward_noalloc(moe_ctx *ctx, const moe_desc *desc 
 
 /* ---------------------------------------------------------------------------
  * Operators next to the layer: RMS norm, the paged KV cache, attention over
- * it.  They need no moe_ctx; the conventions above hold (device pointers,
+ * it; products in E4M3 with a scale per block of 128; norms of queries and keys
+ * for each head with the rotation by position; log probabilities of tokens.
+ * They need no moe_ctx; the conventions above hold (device pointers,
  * 16-byte alignment, asynchronous, arguments checked first, no allocation,
  * bit-identical results from run to run).  A call with zero rows is a no-op
  * that returns MOE_OK. */
@@ -413,6 +415,104 @@ MOE_API moe_status moe_attention(const moe_kv_cache *cache /* host */, const moe
                          const void *q, int64_t q_row, int64_t q_head, int32_t heads, float scale,
                          int32_t window, int32_t sinks, void *out, void *ws, size_t ws_bytes,
                          void *stream);
+
+/* Norms of queries and keys for each head, and their rotation by position:
+ *
+ *   n = x / sqrt(mean(x^2) + eps) * weight                    (over one head)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i],
+ *
+ * for the pairs i < rotary_dim / 2 of elements (i, i + rotary_dim / 2), or with
+ * `interleaved` the neighbours (2i, 2i + 1); elements from rotary_dim on are
+ * normed only.  With norm_after the rotation comes first (the weight then
+ * multiplies what is turned already; the mean is the same).  Angles are held in 64 bits,
+ * sines and cosines rounded to fp32, the rest is fp32; one rounding to the output.
+ *
+ * dtype: MOE_F32 or MOE_BF16 of q, k, v, the weights [head_dim] and the outputs.
+ * head_dim 64, 128 or 256; rotary_dim from 2 to head_dim, even, without
+ * `interleaved` a multiple of 16.  inv_freq: [rotary_dim / 2] fp64. */
+typedef struct moe_head_norm {
+  const void *q_weight, *k_weight;
+  const double *inv_freq;
+  int32_t head_dim, rotary_dim, interleaved, norm_after, dtype;
+  float eps;
+} moe_head_norm;
+
+/* q: [rows][heads][head_dim], k: [rows][kv_heads][head_dim], row and head strides
+ * as for moe_kv_write; positions [rows].  q_out, k_out: contiguous, of the same
+ * shapes. */
+MOE_API moe_status moe_head_norm_rope(const moe_head_norm *norm /* host */, const void *q, int64_t q_row,
+                              int64_t q_head, int32_t heads, const void *k, int64_t k_row,
+                              int64_t k_head, int32_t kv_heads, const int32_t *positions,
+                              int32_t rows, void *q_out, void *k_out, void *stream);
+/* The same for the rows of a batch at their positions, with the turned keys and the
+ * values v written into the cache, as moe_kv_write would (an MX-fp8 cache takes
+ * the codes of the keys before their rounding to bf16).  q_out: zeros for rows of no sequence,
+ * before its start or past its table; keys and values of rows without a page are
+ * dropped.  The norm's dtype is that of the cache's activations, its head_dim the
+ * cache's. */
+MOE_API moe_status moe_head_norm_rope_write(const moe_head_norm *norm /* host */, const moe_kv_cache *cache /* host */,
+                                    const moe_kv_batch *batch /* host */, const void *q,
+                                    int64_t q_row, int64_t q_head, int32_t heads, const void *k,
+                                    int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                                    int64_t v_head, void *q_out, void *stream);
+
+/* Product of activations [rows, k] with weights [n, k] in E4M3, fp32 scales: one
+ * per row and 128 columns of the activations, one per 128 x 128 of the weights (the
+ * last blocks may be smaller):
+ *
+ *   y[r][j] = sum_b x_scale[r][b] w_scale[j / 128][b] sum_{c in block b} xq[r][c] wq[j][c]
+ *
+ * accumulated in fp32, rounded once.  A block's scale is fp32(max|v| / 448), at least
+ * 2^-126, 0 for zeros; its codes are E4M3 of v / scale (the exact quotient, round to
+ * nearest even).  A block with an infinity or NaN gets a NaN scale and NaN codes, which
+ * make every sum they enter NaN.
+ *
+ * Codes are kept packed: blocks of 16 rows x 128 columns, 2048 bytes,
+ * [rows / 16][cols / 128], both counts rounded up and filled with zeros; in a block
+ * byte 1024 h + 16 l + i holds row l % 16, column 32 (l / 16) + 16 h + i.
+ * moe_block_packed_bytes: their size (0: invalid).  Activation scales are
+ * [cols / 128][rows rounded up to 16], weight scales [n / 128][k / 128].
+ * rows, n, k up to 2^30. */
+MOE_API size_t moe_block_packed_bytes(int32_t rows, int32_t cols);
+/* Activations x (MOE_F32 or MOE_BF16, any alignment of an element and row stride;
+ * 16 bytes are faster) to packed codes and scales. */
+MOE_API moe_status moe_block_quantize(const void *x, int dtype, int64_t row_stride, int32_t rows, int32_t cols,
+                              uint8_t *q, float *scale, void *stream);
+/* Weights to packed codes: MOE_F32 or MOE_BF16 are quantised, their scales written;
+ * MOE_FP8 are E4M3 codes already (with scales of the caller's; scale is not
+ * used). */
+MOE_API moe_status moe_block_pack(const void *w, int dtype, int64_t row_stride, int32_t n, int32_t k,
+                          uint8_t *q, float *scale, void *stream);
+/* out [rows][n] contiguous, MOE_F32 or MOE_BF16.  x (MOE_F32 or MOE_BF16) is
+ * quantised into ws first; with xq and xq_scale (of moe_block_quantize) x is
+ * not used and no workspace is needed. */
+MOE_API size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k);
+MOE_API moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, int32_t k,
+                            const void *x, int x_dtype, int64_t x_stride, const uint8_t *xq,
+                            const float *xq_scale, int32_t rows, void *out, int out_dtype,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/* Log probabilities of given tokens, with the entropy of their distribution and its
+ * best alternatives, from rows of logits (MOE_F32 or MOE_BF16; row stride in elements,
+ * any alignment of an element):
+ *
+ *   logprob[r] = x[r][tokens[r]] - log sum_j e^x[r][j],   entropy[r] = -sum_j p_j log p_j
+ *   top_token[r][0 .. top - 1]: the tokens of the largest logits, in descending order,
+ *   equal ones by their index; top_logprob: theirs.
+ *
+ * Logits of -infinity have no part in it and the log probability -infinity, as has a
+ * token outside [0, vocab).  A row of nothing else gives -infinity everywhere
+ * and the entropy 0, one with a NaN or +infinity NaN; among the alternatives
+ * NaN come last.  tokens: 4 or 8 bytes each (token_bytes).  top: 0 (top_logprob and
+ * top_token are not used) to min(vocab, 64).  Sums in fp32.  ws:
+ * moe_token_logprobs_workspace_bytes() bytes (0: none needed, or invalid
+ * arguments). */
+#define MOE_LOGPROBS_MAX_TOP 64
+MOE_API size_t moe_token_logprobs_workspace_bytes(int dtype, int32_t rows, int32_t vocab, int32_t top);
+MOE_API moe_status moe_token_logprobs(const void *logits, int dtype, int64_t row_stride, const void *tokens,
+                              int32_t token_bytes, int32_t rows, int32_t vocab, int32_t top,
+                              float *logprob, float *entropy, float *top_logprob,
+                              int32_t *top_token, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

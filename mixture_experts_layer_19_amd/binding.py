@@ -27,7 +27,10 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_status_string", "moe_ctx_la
            "moe_layer_ws_topk", "moe_ctx_set_profiling", "moe_ctx_stage_ms",
            "moe_layer_forward_quantized", "moe_layer_forward_noalloc",
            "moe_rms_norm", "moe_kv_write", "moe_kv_read", "moe_attention_workspace_bytes",
-           "moe_attention")
+           "moe_attention", "moe_head_norm_rope", "moe_head_norm_rope_write",
+           "moe_block_packed_bytes", "moe_block_quantize", "moe_block_pack",
+           "moe_block_linear_workspace_bytes", "moe_block_linear",
+           "moe_token_logprobs_workspace_bytes", "moe_token_logprobs")
 MOE_NO_QUANT = -1
 STAGES = ("route", "mx_quant", "permute", "gate_up", "down", "shared_gate_up", "shared_down",
           "combine")
@@ -61,6 +64,14 @@ class MoeKvBatch(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p), ("seqs", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("max_rows", ctypes.c_int32)]
+
+
+class MoeHeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm_after", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -111,6 +122,19 @@ def lib():
             "moe_attention_workspace_bytes": ([P, P, I32, I32, I32], S),
             "moe_attention": ([P, P, P, I64, I64, I32, ctypes.c_float, I32, I32, P, P, S, P],
                               ctypes.c_int),
+            "moe_head_norm_rope": ([P, P, I64, I64, I32, P, I64, I64, I32, P, I32, P, P, P],
+                                   ctypes.c_int),
+            "moe_head_norm_rope_write": ([P, P, P, P, I64, I64, I32, P, I64, I64, P, I64, I64, P, P],
+                                         ctypes.c_int),
+            "moe_block_packed_bytes": ([I32, I32], S),
+            "moe_block_quantize": ([P, ctypes.c_int, I64, I32, I32, P, P, P], ctypes.c_int),
+            "moe_block_pack": ([P, ctypes.c_int, I64, I32, I32, P, P, P], ctypes.c_int),
+            "moe_block_linear_workspace_bytes": ([I32, I32, I32], S),
+            "moe_block_linear": ([P, P, I32, I32, P, ctypes.c_int, I64, P, P, I32, P, ctypes.c_int, P,
+                                  S, P], ctypes.c_int),
+            "moe_token_logprobs_workspace_bytes": ([ctypes.c_int, I32, I32, I32], S),
+            "moe_token_logprobs": ([P, ctypes.c_int, I64, P, I32, I32, I32, I32, P, P, P, P, P, S, P],
+                                   ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -278,3 +302,52 @@ def moe_attention(cache: MoeKvCache, batch: MoeKvBatch, q, q_row, q_head, heads,
     _check(lib().moe_attention(ctypes.byref(cache), ctypes.byref(batch), _ptr(q), q_row, q_head,
                                heads, scale, window, sinks, _ptr(out), _ptr(ws), ws_bytes,
                                _stream(stream)))
+
+
+def moe_head_norm_rope(norm: MoeHeadNorm, q, q_row, q_head, heads, k, k_row, k_head, kv_heads,
+                       positions, rows, q_out, k_out, stream=None):
+    _check(lib().moe_head_norm_rope(ctypes.byref(norm), _ptr(q), q_row, q_head, heads, _ptr(k), k_row,
+                                    k_head, kv_heads, _ptr(positions), rows, _ptr(q_out), _ptr(k_out),
+                                    _stream(stream)))
+
+
+def moe_head_norm_rope_write(norm: MoeHeadNorm, cache: MoeKvCache, batch: MoeKvBatch, q, q_row, q_head,
+                             heads, k, k_row, k_head, v, v_row, v_head, q_out, stream=None):
+    _check(lib().moe_head_norm_rope_write(ctypes.byref(norm), ctypes.byref(cache), ctypes.byref(batch),
+                                          _ptr(q), q_row, q_head, heads, _ptr(k), k_row, k_head, _ptr(v),
+                                          v_row, v_head, _ptr(q_out), _stream(stream)))
+
+
+def moe_block_packed_bytes(rows: int, cols: int) -> int:
+    return lib().moe_block_packed_bytes(rows, cols)
+
+
+def moe_block_quantize(x, dtype, row_stride, rows, cols, q, scale, stream=None):
+    _check(lib().moe_block_quantize(_ptr(x), dtype, row_stride, rows, cols, _ptr(q), _ptr(scale),
+                                    _stream(stream)))
+
+
+def moe_block_pack(w, dtype, row_stride, n, k, q, scale=None, stream=None):
+    _check(lib().moe_block_pack(_ptr(w), dtype, row_stride, n, k, _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def moe_block_linear_workspace_bytes(rows: int, n: int, k: int) -> int:
+    return lib().moe_block_linear_workspace_bytes(rows, n, k)
+
+
+def moe_block_linear(wq, w_scale, n, k, x, x_dtype, x_stride, xq, xq_scale, rows, out, out_dtype, ws,
+                     ws_bytes, stream=None):
+    _check(lib().moe_block_linear(_ptr(wq), _ptr(w_scale), n, k, _ptr(x), x_dtype, x_stride, _ptr(xq),
+                                  _ptr(xq_scale), rows, _ptr(out), out_dtype, _ptr(ws), ws_bytes,
+                                  _stream(stream)))
+
+
+def moe_token_logprobs_workspace_bytes(dtype: int, rows: int, vocab: int, top: int) -> int:
+    return lib().moe_token_logprobs_workspace_bytes(dtype, rows, vocab, top)
+
+
+def moe_token_logprobs(logits, dtype, row_stride, tokens, token_bytes, rows, vocab, top, logprob, entropy,
+                       top_logprob, top_token, ws, ws_bytes, stream=None):
+    _check(lib().moe_token_logprobs(_ptr(logits), dtype, row_stride, _ptr(tokens), token_bytes, rows, vocab,
+                                    top, _ptr(logprob), _ptr(entropy), _ptr(top_logprob), _ptr(top_token),
+                                    _ptr(ws), ws_bytes, _stream(stream)))

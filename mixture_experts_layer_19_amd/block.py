@@ -1,6 +1,8 @@
 """The operators next to the MoE layer in its decoder block: RMS norm with the
-residual's addition and an 8-bit output, the paged KV cache, and attention of
-new tokens over that cache.
+residual's addition and an 8-bit output, the matrix product in 8 bits with a
+scale per block of 128, the norms of queries and keys with their rotation, the
+paged KV cache, attention of new tokens over that cache, and the log
+probabilities of tokens behind the last block.
 
 Plumbing only, as in :mod:`.layer`: torch holds device memory and streams, the
 HIP library (through :mod:`.binding`) does the arithmetic.  Calls run on the
@@ -14,6 +16,11 @@ are read on the device when the kernels run.
     o = cache.attention(batch, q, window=4096, sinks=16)
     norm = RMSNorm(weight, quant="mxfp8")
     residual, y, q8, scale = norm(x, residual)
+
+    qkv = BlockLinear(w_qkv)(y).unflatten(1, (-1, 128))
+    q, k, v = qkv.split((heads, kv_heads, kv_heads), 1)
+    q = HeadNormRope(q_weight, k_weight, base=1e4).write(cache, batch, q, k, v)
+    logprob, entropy, _, _ = token_logprobs(BlockLinear(w_head, out_dtype=torch.float32)(y), tokens)
 
 What cannot be seen from the host (the contents of the page table, offsets and
 lengths) is not checked: whatever it is, no access leaves the tensors.
@@ -305,3 +312,274 @@ class PagedKVCache(_Bound):
         if rc:
             B._check(rc)
         return out
+
+
+class HeadNormRope(_Bound):
+    """RMS norm of each head of the queries and keys and their rotation by position,
+    in one pass.
+
+    q_weight, k_weight [head_dim] (float32 or bfloat16, the type of q, k and v;
+    head_dim 64, 128 or 256).  Pairs of elements (i, i + rotary_dim / 2), or with
+    interleaved (2i, 2i + 1), turn by position * inv_freq[i]; inv_freq:
+    [rotary_dim / 2], base ** (-2i / rotary_dim) if not given; rotary_dim: head_dim
+    if not given (a multiple of 16, with interleaved of 2), the elements behind it are
+    normed only.  norm_after: the weights multiply what is turned already."""
+
+    _bound = frozenset(("q_weight", "k_weight", "inv_freq", "head_dim", "rotary_dim", "interleaved", "norm_after",
+                        "eps", "dtype", "device", "c"))
+
+    def __init__(self, q_weight: torch.Tensor, k_weight: torch.Tensor, base: float = 10000.0,
+                 rotary_dim: Optional[int] = None, inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 interleaved: bool = False, norm_after: bool = False):
+        for w in (q_weight, k_weight):
+            _require(w.dim() == 1 and w.is_contiguous() and w.shape == q_weight.shape and w.dtype == q_weight.dtype
+                     and w.device == q_weight.device, "weights must be contiguous vectors of one size, type and device")
+        _require(q_weight.dtype in _ACT, "weights must be float32 or bfloat16, got %s" % q_weight.dtype)
+        head_dim = q_weight.numel()
+        _require(head_dim in (64, 128, 256), "head_dim must be 64, 128 or 256, got %d" % head_dim)
+        self.device = _device(q_weight)
+        if inv_freq is not None:
+            _require(inv_freq.dim() == 1 and inv_freq.device == self.device
+                     and inv_freq.dtype in (torch.float32, torch.float64),
+                     "inv_freq must be a float32 or float64 vector on %s" % self.device)
+            _require(rotary_dim is None or rotary_dim == 2 * inv_freq.numel(),
+                     "inv_freq must have rotary_dim / 2 elements")
+            rotary_dim = 2 * inv_freq.numel()
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        _require(0 < rotary_dim <= head_dim and rotary_dim % (2 if interleaved else 16) == 0,
+                 "rotary_dim must be a multiple of %d up to %d, got %d" % (2 if interleaved else 16, head_dim, rotary_dim))
+        _require(eps >= 0.0, "eps must not be negative")
+        if inv_freq is None:
+            _require(base > 0.0, "base must be positive")
+            at = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+            inv_freq = (float(base) ** (at / -rotary_dim)).to(self.device)
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.inv_freq = inv_freq.to(torch.float64).contiguous()
+        self.head_dim, self.rotary_dim, self.eps = head_dim, rotary_dim, float(eps)
+        self.interleaved, self.norm_after, self.dtype = bool(interleaved), bool(norm_after), q_weight.dtype
+        self.c = B.MoeHeadNorm(q_weight.data_ptr(), k_weight.data_ptr(), self.inv_freq.data_ptr(), head_dim,
+                               rotary_dim, int(interleaved), int(norm_after), _ACT[q_weight.dtype], self.eps)
+        self._ref = ctypes.byref(self.c)
+        lib = B.lib()
+        self._turn, self._write = lib.moe_head_norm_rope, lib.moe_head_norm_rope_write
+
+    def _check(self, t, rows, what):
+        if t.dim() != 3 or t.shape[0] != rows or t.shape[1] == 0 or t.shape[2] != self.head_dim \
+                or t.dtype != self.dtype or t.device != self.device:
+            raise ValueError("%s must be [%d, heads, %d] of %s on %s, got %s of %s on %s"
+                             % (what, rows, self.head_dim, self.dtype, self.device, list(t.shape), t.dtype, t.device))
+        if t.stride(2) != 1:
+            raise ValueError("%s must be contiguous along head_dim" % what)
+
+    def __call__(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, stream=None):
+        """(q, k) [rows, heads, head_dim] and [rows, kv_heads, head_dim] (row and head
+        strides in whole 16-byte pieces), normed and turned to positions [rows] int32."""
+        rows = q.shape[0]
+        self._check(q, rows, "q")
+        self._check(k, rows, "k")
+        if positions.shape != (rows,) or positions.dtype != torch.int32 or not positions.is_contiguous() \
+                or positions.device != self.device:
+            raise ValueError("positions must be contiguous int32 [%d] on %s" % (rows, self.device))
+        _require(rows <= _INT32, "rows must be below 2^31")
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self(q, k, positions)
+        h, g, d = q.shape[1], k.shape[1], self.head_dim
+        q_out = torch.empty_strided((rows, h, d), (h * d, d, 1), dtype=self.dtype, device=self.device)
+        k_out = torch.empty_strided((rows, g, d), (g * d, d, 1), dtype=self.dtype, device=self.device)
+        rc = self._turn(self._ref, q.data_ptr(), q.stride(0), q.stride(1), h, k.data_ptr(), k.stride(0), k.stride(1),
+                        g, positions.data_ptr(), rows, q_out.data_ptr(), k_out.data_ptr(),
+                        _raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+        return q_out, k_out
+
+    def write(self, cache: PagedKVCache, batch: KVBatch, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
+              stream=None) -> torch.Tensor:
+        """q [rows, heads, head_dim] at the batch's positions; its keys, normed and
+        turned, and the values v go into the cache in the same pass."""
+        self._check(q, batch.rows, "q")
+        _require(self.head_dim == cache.head_dim, "the norm's head_dim is %d, the cache's %d"
+                 % (self.head_dim, cache.head_dim))
+        cache._check(batch, k, cache.kv_heads, "k")
+        cache._check(batch, v, cache.kv_heads, "v")
+        _require(self.dtype == cache.act_dtype and self.device == cache.device,
+                 "the norm and the cache's activations differ in type or device")
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self.write(cache, batch, q, k, v)
+        rows, h, d = q.shape
+        out = torch.empty_strided((rows, h, d), (h * d, d, 1), dtype=self.dtype, device=self.device)
+        rc = self._write(self._ref, cache._ref, batch._ref, q.data_ptr(), q.stride(0), q.stride(1), h, k.data_ptr(),
+                         k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), out.data_ptr(),
+                         _raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+        return out
+
+
+class BlockCodes(NamedTuple):
+    q: torch.Tensor        # packed E4M3 codes, uint8
+    scale: torch.Tensor    # float32 [in_features / 128, rows up to a multiple of 16]
+    rows: int
+
+
+class BlockLinear(_Bound):
+    """y = x W^T in E4M3 with one fp32 scale per 128 x 128 of the weights and one per
+    row and 128 columns of x, accumulated in fp32.
+
+    weight [out_features, in_features]: float32 or bfloat16, quantised here (a block's
+    scale is max / 448); or E4M3 codes (uint8 or float8_e4m3fn) with their scale
+    [out_features / 128, in_features / 128] float32, rounded up.  Either is packed
+    once; codes of quantised weights are not kept otherwise.  dtype: x's, float32 or bfloat16; out_dtype:
+    y's, dtype if not given.  Any sizes."""
+
+    _bound = frozenset(("q", "scale", "out_features", "in_features", "dtype", "out_dtype", "device"))
+
+    def __init__(self, weight: torch.Tensor, scale: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
+                 out_dtype=None):
+        out_dtype = dtype if out_dtype is None else out_dtype
+        _require(dtype in _ACT and out_dtype in _ACT, "dtype and out_dtype must be float32 or bfloat16")
+        _require(weight.dim() == 2 and weight.numel() > 0, "weight must be [out_features, in_features]")
+        n, k = weight.shape
+        _require(max(n, k) <= 1 << 30, "features must not be above 2^30")
+        self.device = _device(weight)
+        codes = weight.dtype in (torch.uint8, torch.float8_e4m3fn)
+        _require(codes or weight.dtype in _ACT, "weight must be float32, bfloat16 or E4M3 codes, got %s" % weight.dtype)
+        _require(codes == (scale is not None), "a scale goes with E4M3 codes only, and they with a scale")
+        shape = (-(-n // 128), -(-k // 128))
+        if codes:
+            _require(tuple(scale.shape) == shape and scale.dtype == torch.float32 and scale.is_contiguous()
+                     and scale.device == self.device, "scale must be contiguous float32 %s on %s"
+                     % (list(shape), self.device))
+        if weight.stride(1) != 1 and k != 1:
+            weight = weight.contiguous()
+        self.out_features, self.in_features, self.dtype, self.out_dtype = n, k, dtype, out_dtype
+        lib = B.lib()
+        with torch.cuda.device(self.device):
+            self.scale = scale if codes else torch.empty(shape, dtype=torch.float32, device=self.device)
+            self.q = torch.empty(lib.moe_block_packed_bytes(n, k), dtype=torch.uint8, device=self.device)
+            B.moe_block_pack(weight, B.MOE_FP8 if codes else _ACT[weight.dtype], weight.stride(0), n, k, self.q,
+                             self.scale, _raw_stream(self.device.index))
+        self._in, self._out = _ACT[dtype], _ACT[out_dtype]
+        self._w, self._ws = self.q.data_ptr(), self.scale.data_ptr()
+        self._call, self._quantize = lib.moe_block_linear, lib.moe_block_quantize
+        self._bytes = lib.moe_block_linear_workspace_bytes
+
+    def _check(self, x):
+        if x.dim() != 2 or x.shape[1] != self.in_features or x.dtype != self.dtype or x.device != self.device:
+            raise ValueError("expected [rows, %d] of %s on %s, got %s of %s on %s"
+                             % (self.in_features, self.dtype, self.device, list(x.shape), x.dtype, x.device))
+        if x.stride(1) != 1 and self.in_features != 1:
+            raise ValueError("rows must be contiguous")
+        if x.shape[0] > 1 << 30:
+            raise ValueError("%d rows are more than 2^30" % x.shape[0])
+
+    def quantize(self, x: torch.Tensor, *, stream=None) -> BlockCodes:
+        """x's codes, for products that share it (weights of the same in_features)."""
+        self._check(x)
+        other = _elsewhere(self.device.index, stream)
+        if other is not None:
+            with other:
+                return self.quantize(x)
+        rows, k = x.shape
+        q = torch.empty(B.lib().moe_block_packed_bytes(rows, k), dtype=torch.uint8, device=self.device)
+        scale = torch.empty((-(-k // 128), -(-rows // 16) * 16), dtype=torch.float32, device=self.device)
+        B.moe_block_quantize(x, self._in, x.stride(0), rows, k, q, scale, _raw_stream(self.device.index))
+        return BlockCodes(q, scale, rows)
+
+    def __call__(self, x: Optional[torch.Tensor] = None, *, codes: Optional[BlockCodes] = None,
+                 stream=None) -> torch.Tensor:
+        """x [rows, in_features], or its codes of :meth:`quantize`, -> [rows, out_features]."""
+        k, dev = self.in_features, self.device
+        if codes is None:
+            if x is None:
+                raise ValueError("x or its codes are needed")
+            self._check(x)
+            rows = x.shape[0]
+        else:
+            if x is not None:
+                raise ValueError("x and its codes exclude each other")
+            rows = codes.rows
+            want = (-(-k // 128), -(-rows // 16) * 16)
+            for t, shape, kind in ((codes.q, (want[0] * want[1] * 128,), torch.uint8),
+                                   (codes.scale, want, torch.float32)):
+                if tuple(t.shape) != shape or t.dtype != kind or not t.is_contiguous() or t.device != dev:
+                    raise ValueError("codes must be those of [rows, %d] on %s" % (k, dev))
+        other = _elsewhere(dev.index, stream)
+        if other is not None:
+            with other:
+                return self(x, codes=codes)
+        n = self.out_features
+        out = torch.empty_strided((rows, n), (n, 1), dtype=self.out_dtype, device=dev)
+        xp = xs = qp = sp = wp = 0
+        size, ws = 0, None
+        if codes is not None:
+            qp, sp = codes.q.data_ptr(), codes.scale.data_ptr()
+        else:
+            xp, xs, size = x.data_ptr(), x.stride(0), self._bytes(rows, n, k)
+            if size:
+                ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=dev)
+                wp = ws.data_ptr()
+        rc = self._call(self._w, self._ws, n, k, xp, self._in, xs, qp, sp, rows, out.data_ptr(), self._out, wp, size,
+                        _raw_stream(dev.index))
+        if rc:
+            B._check(rc)
+        return out
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: torch.Tensor                  # [rows] float32
+    entropy: torch.Tensor                  # [rows] float32
+    top_logprob: Optional[torch.Tensor]    # [rows, top] float32, best first (None without alternatives)
+    top_token: Optional[torch.Tensor]      # [rows, top] int32
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, stream=None) -> TokenLogprobs:
+    """Log probabilities of tokens [rows] (int32 or int64) under logits [rows, vocab]
+    (float32 or bfloat16, rows contiguous inside), the entropy of each row, and the
+    `top` (up to 64) best tokens, equal logits by their index.
+
+    Masked logits are -inf: no part of the distribution, log probability -inf, as a
+    token outside the vocabulary; a row of nothing else has the entropy 0.  A row with a
+    NaN or +inf gives NaN."""
+    if logits.dim() != 2 or logits.dtype not in _ACT:
+        raise ValueError("logits must be [rows, vocab] of float32 or bfloat16, got %s of %s"
+                         % (list(logits.shape), logits.dtype))
+    rows, vocab = logits.shape
+    dev = _device(logits)
+    if vocab == 0 or max(rows, vocab) > _INT32:
+        raise ValueError("rows must be below 2^31, the vocabulary from 1 to 2^31 - 1")
+    if logits.stride(1) != 1 and vocab != 1:
+        raise ValueError("rows must be contiguous")
+    if tokens.shape != (rows,) or tokens.dtype not in (torch.int32, torch.int64) or not tokens.is_contiguous() \
+            or tokens.device != dev:
+        raise ValueError("tokens must be contiguous int32 or int64 [%d] on %s, got %s of %s on %s"
+                         % (rows, dev, list(tokens.shape), tokens.dtype, tokens.device))
+    if not 0 <= top <= min(vocab, 64):
+        raise ValueError("top must be from 0 to %d, got %d" % (min(vocab, 64), top))
+    other = _elsewhere(dev.index, stream)
+    if other is not None:
+        with other:
+            return token_logprobs(logits, tokens, top)
+    lib, dtype, new = B.lib(), _ACT[logits.dtype], torch.empty_strided
+    logprob = new((rows,), (1,), dtype=torch.float32, device=dev)
+    entropy = new((rows,), (1,), dtype=torch.float32, device=dev)
+    values = ids = ws = None
+    vp = ip = wp = 0
+    if top:
+        values = new((rows, top), (top, 1), dtype=torch.float32, device=dev)
+        ids = new((rows, top), (top, 1), dtype=torch.int32, device=dev)
+        vp, ip = values.data_ptr(), ids.data_ptr()
+    size = lib.moe_token_logprobs_workspace_bytes(dtype, rows, vocab, top)
+    if size:
+        ws = new((size,), (1,), dtype=torch.uint8, device=dev)
+        wp = ws.data_ptr()
+    rc = lib.moe_token_logprobs(logits.data_ptr(), dtype, logits.stride(0), tokens.data_ptr(), tokens.element_size(),
+                                rows, vocab, top, logprob.data_ptr(), entropy.data_ptr(), vp, ip, wp, size,
+                                _raw_stream(dev.index))
+    if rc:
+        B._check(rc)
+    return TokenLogprobs(logprob, entropy, values, ids)

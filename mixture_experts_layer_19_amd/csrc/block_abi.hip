@@ -93,6 +93,56 @@ bool few_rows(const AttnArgs &a) {
   return (long long)a.c.max_rows * a.group <= 32 || (a.c.fmt == FMT_F32 && a.c.head_dim == 256) || a.c.page_shift < 3;
 }
 
+constexpr int32_t kMostBlocked = 1 << 30;       // rows and columns of a block-scaled matrix
+
+bool float_type(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+bool blocked(int32_t n) { return n > 0 && n <= kMostBlocked; }
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+int64_t rows16(int64_t n) { return (n + 15) / 16 * 16; }
+size_t scale_bytes(int32_t rows, int32_t cols) { return (size_t)(blocks_of(cols) * rows16(rows) * 4); }
+
+// Check what both head norms take and put it in the kernel's form (a.c.rows,
+// kv_heads and head_dim are set before).
+moe_status head_norm_args(const moe_head_norm *n, int heads, const void *q, int64_t q_row, int64_t q_head,
+                          const void *k, int64_t k_row, int64_t k_head, const void *q_out, RotateArgs *a) {
+  if (!float_type(n->dtype) || heads <= 0 || !(n->eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (n->rotary_dim < 2 || n->rotary_dim > n->head_dim || n->rotary_dim % (n->interleaved ? 2 : 16))
+    return MOE_ERR_INVALID_ARG;
+  if (n->head_dim != 64 && n->head_dim != 128 && n->head_dim != 256) return MOE_ERR_UNSUPPORTED;
+  if (heads > 65536) return MOE_ERR_UNSUPPORTED;
+  if (a->c.rows == 0) return MOE_OK;
+  for (const void *p : {n->q_weight, n->k_weight, q, k, q_out})
+    if (!p || !al(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (!n->inv_freq || !al(n->inv_freq, 8)) return MOE_ERR_INVALID_ARG;
+  a->c.fmt = n->dtype == MOE_F32 ? FMT_F32 : a->c.fmt == FMT_MX8 ? FMT_MX8 : FMT_BF16;
+  if (!strides_ok(a->c, heads, q_row, q_head) || !strides_ok(a->c, a->c.kv_heads, k_row, k_head))
+    return MOE_ERR_INVALID_ARG;
+  a->q = q;
+  a->k = k;
+  a->q_row = q_row;
+  a->q_head = q_head;
+  a->k_row = k_row;
+  a->k_head = k_head;
+  a->q_weight = n->q_weight;
+  a->k_weight = n->k_weight;
+  a->inv_freq = n->inv_freq;
+  a->heads = heads;
+  a->rotary = n->rotary_dim;
+  a->interleaved = n->interleaved != 0;
+  a->after = n->norm_after != 0;
+  a->eps = n->eps;
+  a->q_out = const_cast<void *>(q_out);
+  return MOE_OK;
+}
+
+bool logprob_args(int dtype, int32_t rows, int32_t vocab, int32_t top) {
+  return float_type(dtype) && rows >= 0 && vocab > 0 && top >= 0 && top <= kLogprobTop && top <= vocab;
+}
+size_t logprob_ws(int dtype, int32_t rows, int32_t vocab, int32_t top) {
+  const int parts = logprob_parts(rows, vocab, dtype == MOE_BF16);
+  return parts == 1 ? 0 : (size_t)rows * parts * (16 + 8 * (size_t)top);
+}
+
 size_t workspace(const AttnArgs &a) {
   if (a.c.rows <= 0) return 0;
   return few_rows(a) ? attn_rows_ws_bytes(a) : attn_tile_ws_bytes(a);
@@ -179,6 +229,121 @@ moe_status moe_attention(const moe_kv_cache *cache, const moe_kv_batch *batch, c
   a.grid = 0;
   const hipStream_t s = (hipStream_t)stream;
   return done(few_rows(a) ? launch_attn_rows(a, s) : launch_attn_tile(a, s));
+}
+
+moe_status moe_head_norm_rope(const moe_head_norm *norm, const void *q, int64_t q_row, int64_t q_head,
+                              int32_t heads, const void *k, int64_t k_row, int64_t k_head,
+                              int32_t kv_heads, const int32_t *positions, int32_t rows, void *q_out,
+                              void *k_out, void *stream) {
+  if (!norm || rows < 0 || kv_heads <= 0) return MOE_ERR_INVALID_ARG;
+  if (kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
+  RotateArgs a = {};
+  a.c.rows = rows;
+  a.c.kv_heads = kv_heads;
+  a.c.head_dim = norm->head_dim;
+  moe_status st = head_norm_args(norm, heads, q, q_row, q_head, k, k_row, k_head, q_out, &a);
+  if (st != MOE_OK || rows == 0) return st;
+  if (!positions || !al(positions, 4) || !k_out || !al(k_out, 16)) return MOE_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.k_out = k_out;
+  return done(launch_rotate(a, norm->dtype == MOE_BF16, 0, (hipStream_t)stream));
+}
+
+moe_status moe_head_norm_rope_write(const moe_head_norm *norm, const moe_kv_cache *cache,
+                                    const moe_kv_batch *batch, const void *q, int64_t q_row,
+                                    int64_t q_head, int32_t heads, const void *k, int64_t k_row,
+                                    int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                                    void *q_out, void *stream) {
+  if (!norm) return MOE_ERR_INVALID_ARG;
+  RotateArgs a = {};
+  moe_status st = kv_args(cache, batch, &a.c);
+  if (st != MOE_OK) return st;
+  if (norm->head_dim != cache->head_dim || norm->dtype != (cache->dtype == MOE_F32 ? MOE_F32 : MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  st = head_norm_args(norm, heads, q, q_row, q_head, k, k_row, k_head, q_out, &a);
+  if (st != MOE_OK || a.c.rows == 0) return st;
+  if (!v || !al(v, 16) || !strides_ok(a.c, a.c.kv_heads, v_row, v_head)) return MOE_ERR_INVALID_ARG;
+  a.v = v;
+  a.v_row = v_row;
+  a.v_head = v_head;
+  return done(launch_rotate(a, norm->dtype == MOE_BF16, 1, (hipStream_t)stream));
+}
+
+size_t moe_block_packed_bytes(int32_t rows, int32_t cols) {
+  return blocked(rows) && blocked(cols) ? (size_t)(rows16(rows) * blocks_of(cols) * 128) : 0;
+}
+
+moe_status moe_block_quantize(const void *x, int dtype, int64_t row_stride, int32_t rows, int32_t cols,
+                              uint8_t *q, float *scale, void *stream) {
+  if (!float_type(dtype) || rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+  if (rows > kMostBlocked || cols > kMostBlocked) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !al(x, dtype == MOE_F32 ? 4 : 2) || !q || !al(q, 16) || !scale || !al(scale, 16))
+    return MOE_ERR_INVALID_ARG;
+  return done(launch_block_quantize(x, row_stride, dtype == MOE_BF16, rows, cols, q, scale, (hipStream_t)stream));
+}
+
+moe_status moe_block_pack(const void *w, int dtype, int64_t row_stride, int32_t n, int32_t k, uint8_t *q,
+                          float *scale, void *stream) {
+  if ((!float_type(dtype) && dtype != MOE_FP8) || n <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+  if (n > kMostBlocked || k > kMostBlocked || blocks_of(n) * blocks_of(k) > max_groups(128)) return MOE_ERR_UNSUPPORTED;
+  if (!w || !al(w, dtype == MOE_F32 ? 4 : dtype == MOE_BF16 ? 2 : 1) || !q || !al(q, 16)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_FP8 && (!scale || !al(scale, 4))) return MOE_ERR_INVALID_ARG;
+  const int src = dtype == MOE_FP8 ? FMT_FP8 : dtype == MOE_BF16 ? FMT_BF16 : FMT_F32;
+  return done(launch_block_pack(w, row_stride, src, n, k, q, scale, (hipStream_t)stream));
+}
+
+size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k) {
+  if (!blocked(rows) || !blocked(n) || !blocked(k)) return 0;
+  return moe_block_packed_bytes(rows, k) + scale_bytes(rows, k);
+}
+
+moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, int32_t k, const void *x,
+                            int x_dtype, int64_t x_stride, const uint8_t *xq, const float *xq_scale,
+                            int32_t rows, void *out, int out_dtype, void *ws, size_t ws_bytes, void *stream) {
+  if (rows < 0 || n <= 0 || k <= 0 || !float_type(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!xq != !xq_scale || (!xq && !float_type(x_dtype))) return MOE_ERR_INVALID_ARG;
+  if (rows > kMostBlocked || n > kMostBlocked || k > kMostBlocked) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!wq || !al(wq, 16) || !w_scale || !al(w_scale, 4) || !out || !al(out, 16) || !al(xq, 16) || !al(xq_scale, 16) ||
+      !al(ws, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (!linear_fits(rows, n, k)) return MOE_ERR_UNSUPPORTED;
+  if (!xq) {
+    if (!x || !al(x, x_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_block_linear_workspace_bytes(rows, n, k)) return MOE_ERR_WORKSPACE;
+    uint8_t *q = (uint8_t *)ws;
+    float *scale = (float *)(q + moe_block_packed_bytes(rows, k));
+    const hipError_t err =
+        launch_block_quantize(x, x_stride, x_dtype == MOE_BF16, rows, k, q, scale, (hipStream_t)stream);
+    if (err != hipSuccess) return MOE_ERR_DEVICE;
+    xq = q;
+    xq_scale = scale;
+  }
+  const LinearArgs a = {xq, xq_scale, wq, w_scale, out, rows, n, k};
+  return done(launch_linear(a, out_dtype == MOE_F32, (hipStream_t)stream));
+}
+
+size_t moe_token_logprobs_workspace_bytes(int dtype, int32_t rows, int32_t vocab, int32_t top) {
+  return logprob_args(dtype, rows, vocab, top) ? logprob_ws(dtype, rows, vocab, top) : 0;
+}
+
+moe_status moe_token_logprobs(const void *logits, int dtype, int64_t row_stride, const void *tokens,
+                              int32_t token_bytes, int32_t rows, int32_t vocab, int32_t top, float *logprob,
+                              float *entropy, float *top_logprob, int32_t *top_token, void *ws,
+                              size_t ws_bytes, void *stream) {
+  if (!logprob_args(dtype, rows, vocab, top) || (token_bytes != 4 && token_bytes != 8)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!logits || !al(logits, dtype == MOE_F32 ? 4 : 2) || !tokens || !al(tokens, token_bytes)) return MOE_ERR_INVALID_ARG;
+  if (!logprob || !al(logprob, 4) || !entropy || !al(entropy, 4)) return MOE_ERR_INVALID_ARG;
+  if (top && (!top_logprob || !al(top_logprob, 4) || !top_token || !al(top_token, 4))) return MOE_ERR_INVALID_ARG;
+  if (!al(ws, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t need = logprob_ws(dtype, rows, vocab, top);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  const LogprobArgs a = {logits, row_stride, tokens, dtype == MOE_BF16, token_bytes, rows, vocab, top,
+                         logprob_parts(rows, vocab, dtype == MOE_BF16), logprob, entropy, top_logprob, top_token,
+                         (uint8_t *)ws};
+  return done(launch_logprobs(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -53,6 +53,45 @@ __device__ __forceinline__ uint2 e4m3_to_bf16x4(uint32_t codes, uint32_t sb) {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true)));
 }
 
+// Eight consecutive elements of a row, 16-byte aligned.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, long long i, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint4 u = *(const uint4 *)((const uint16_t *)p + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = *(const float4 *)((const float *)p + i);
+    const float4 b = *(const float4 *)((const float *)p + i + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, long long i, const float (&v)[8]) {
+  if constexpr (BF16) {
+    *(uint4 *)((uint16_t *)p + i) = make_uint4(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]),
+                                               bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7]));
+  } else {
+    *(float4 *)((float *)p + i) = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4 *)((float *)p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+// d rounded to fp32: to nearest, or to odd (towards zero, then the last bit set if
+// anything was cut off), from which one more rounding to fewer bits is as if from d.
+template <bool ODD>
+__device__ __forceinline__ float round_f32(double d) {
+  const float n = (float)d;
+  if constexpr (!ODD) return n;
+  uint32_t u = __float_as_uint(n);
+  u -= fabs((double)n) > fabs(d) ? 1u : 0u;
+  return __uint_as_float(u | ((double)n != d ? 1u : 0u));
+}
+
 // Largest / sum over the two half waves and over the four rows of 16 lanes.
 __device__ __forceinline__ float max_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -1,5 +1,6 @@
 // block_launch.hpp -- host-side launchers of the operators around the MoE
-// layer: RMS norm, the paged KV cache, attention over it (internal).
+// layer: RMS norm, the paged KV cache, attention over it, the block-scaled 8-bit
+// product, head norms with rotation, token log probabilities (internal).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -62,5 +63,55 @@ hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream);
 size_t attn_tile_ws_bytes(const AttnArgs &a);
 bool attn_tile_fits(const AttnArgs &a);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t stream);
+
+// Head norms and rotation (rotate.hip).  Strides in elements.  With positions: keys to
+// k_out; without: rows, positions and places are those of c's batch, keys and values go
+// into its pool.
+struct RotateArgs {
+  KvArgs c;                    // rows, kv_heads, head_dim (and with a cache all of it)
+  const void *q, *k, *v;
+  long long q_row, q_head, k_row, k_head, v_row, v_head;
+  const void *q_weight, *k_weight;             // [head_dim]
+  const double *inv_freq;                      // [rotary / 2]
+  const int32_t *positions;                    // [rows]
+  int heads, rotary, interleaved, after;       // after: the weight multiplies what is turned already
+  float eps;
+  void *q_out, *k_out;                         // contiguous
+};
+hipError_t launch_rotate(const RotateArgs &a, int is_bf16, int into_cache, hipStream_t stream);
+
+// The block-scaled E4M3 product (linear.hip).  Codes of both sides in the packed order,
+// [rows / 16][k / 128] blocks of 2 KiB.
+struct LinearArgs {
+  const uint8_t *q;            // activations
+  const float *q_scale;        // [k / 128][rows, up to a multiple of 16]
+  const uint8_t *w;
+  const float *w_scale;        // [n / 128][k / 128]
+  void *out;                   // [rows][n]
+  int rows, n, k;
+};
+hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, int rows, int cols, uint8_t *q,
+                                 float *scale, hipStream_t stream);
+// src: FMT_F32, FMT_BF16 (scales are written) or FMT_FP8 (codes, which only change places).
+hipError_t launch_block_pack(const void *w, long long stride, int src, int n, int cols, uint8_t *q, float *scale,
+                             hipStream_t stream);
+bool linear_fits(int rows, int n, int k);        // within one launch's workgroups
+hipError_t launch_linear(const LinearArgs &a, int f32_out, hipStream_t stream);
+
+// Token log probabilities (logprobs.hip).
+constexpr int kLogprobTop = 64;                  // alternatives at most
+constexpr int kLogprobParts = 32;                // parts of a row at most
+struct LogprobArgs {
+  const void *logits;          // [rows][vocab], stride in elements
+  long long stride;
+  const void *tokens;          // [rows] of token_bytes
+  int is_bf16, token_bytes, rows, vocab, top, parts;
+  float *logprob, *entropy;    // [rows]
+  float *top_logprob;          // [rows][top]
+  int32_t *top_token;
+  uint8_t *ws;                 // parts > 1: [rows][parts] sums of 16 bytes, then [rows][parts][top] keys of 8
+};
+int logprob_parts(int rows, int vocab, int is_bf16);
+hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t stream);
 
 }  // namespace moe

@@ -24,33 +24,6 @@
 
 namespace moe {
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, long long i, float (&v)[8]) {
-  if constexpr (BF16) {
-    const uint4 u = *(const uint4 *)((const uint16_t *)p + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = *(const float4 *)((const float *)p + i);
-    const float4 b = *(const float4 *)((const float *)p + i + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ void store8(void *p, long long i, const float (&v)[8]) {
-  if constexpr (BF16) {
-    *(uint4 *)((uint16_t *)p + i) = make_uint4(bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]),
-                                               bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7]));
-  } else {
-    *(float4 *)((float *)p + i) = make_float4(v[0], v[1], v[2], v[3]);
-    *(float4 *)((float *)p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
 // n of 8 elements, one at a time
 template <bool BF16>
 __device__ __forceinline__ void load_n(const void *p, long long i, int n, float (&v)[8]) {
@@ -73,16 +46,6 @@ __device__ __forceinline__ void store_n(void *p, long long i, int n, const float
     }
 }
 
-// d rounded to fp32: to nearest, or to odd (towards zero, then the last bit set if
-// anything was cut off), from which one more rounding to fewer bits is as if from d.
-template <bool ODD>
-__device__ __forceinline__ float round_f32(double d) {
-  const float n = (float)d;
-  if constexpr (!ODD) return n;
-  uint32_t u = __float_as_uint(n);
-  u -= fabs((double)n) > fabs(d) ? 1u : 0u;
-  return __uint_as_float(u | ((double)n != d ? 1u : 0u));
-}
 // y of 8 elements: `out` to be stored as the row's type, `code` for the codes (FP8:
 // y by the scale, in 64 bits as y is; the scale's inverse, 8192 x 4096 57.5 us,
 // adds a rounding of 2^-53 to the quotient's, 67.8).

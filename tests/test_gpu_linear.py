@@ -1,0 +1,224 @@
+"""The block-scaled E4M3 product against a plain one in 64 bits: codes and scales bit
+for bit, products within the bound of their additions."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from mixture_experts_layer_19_amd import binding as B
+from mixture_experts_layer_19_amd import block
+
+import _answer as R
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rows_of(g, rows, k, dtype):
+    x = torch.randn(rows, k, generator=g) * torch.exp(2 * torch.randn(1, k, generator=g))
+    return x.to(dtype)
+
+
+def weight_of(g, n, k):
+    codes = (120 * torch.randn(n, k, generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    scale = (0.5 + torch.rand(-(-n // 128), -(-k // 128), generator=g)) / (120 * math.sqrt(k))
+    return codes, scale
+
+
+def check(lin, x, wq, ws, y):
+    xq, xs = R.quantize_rows(x)
+    want, bound = R.linear_ref(xq, xs, wq, ws, y.dtype)
+    assert y.shape == want.shape
+    off = (y.cpu().double() - want).abs()
+    assert (off <= bound + 1e-38).all(), float((off / (bound + 1e-38)).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,k", [(1, 1), (1, 128), (3, 127), (16, 129), (17, 256), (33, 640), (40, 1000)])
+def test_codes(dtype, rows, k):
+    g = gen(rows + k)
+    x = rows_of(g, rows, k, dtype)
+    x[0, :] = 0
+    if rows > 2:
+        x[2] *= 2.0 ** -100
+    lin = block.BlockLinear(torch.ones(4, k, device="cuda", dtype=BF16), dtype=dtype)
+    c = lin.quantize(x.cuda())
+    q, s = R.quantize_rows(x)
+    got = R.unpack(c.q.cpu(), rows, k)
+    assert c.rows == rows and torch.equal(c.scale.cpu()[:, :rows].T, s)
+    assert torch.equal(got[:rows, :k].view(torch.float8_e4m3fn).double(), q)
+    assert (got[rows:] == 0).all() and ((got[:, k:] & 0x7F) == 0).all() and (c.scale.cpu()[:, rows:] == 0).all()
+
+
+def test_codes_next_to_borders():
+    """Quotients on and next to the borders of two codes, for scales of which the
+    inverse is not exact: a border itself goes to the even code."""
+    xs = []
+    for top in (140.0, 1.09375, 448.0, 7.0 / 3, 3.3e-5, 133.0):
+        s = float(torch.tensor(top) / 448.0)
+        row = [top]
+        for m in range(17, 32, 2):               # borders between codes of 4 bits
+            for e in (-3, 0, 3):
+                b = torch.tensor(m * 2.0 ** e * s, dtype=F32)
+                row += [float(b), float(torch.nextafter(b, torch.tensor(math.inf))),
+                        float(torch.nextafter(b, torch.tensor(0.0)))]
+        row = [v for v in row if abs(v) <= top][:128]
+        xs.append(torch.tensor(row + [0.0] * (128 - len(row))))
+    x = torch.stack(xs)
+    lin = block.BlockLinear(torch.ones(4, 128, device="cuda", dtype=BF16), dtype=F32)
+    c = lin.quantize(x.cuda())
+    q, s = R.quantize_rows(x)
+    assert torch.equal(c.scale.cpu()[:, :len(xs)].T, s)
+    assert torch.equal(R.unpack(c.q.cpu(), len(xs), 128)[:len(xs)].view(torch.float8_e4m3fn).double(), q)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,k", [(1, 1), (5, 130), (128, 128), (129, 257), (300, 64)])
+def test_weights_are_quantised(dtype, n, k):
+    w = rows_of(gen(n * k), n, k, dtype)
+    w[0, 0] = 50.0
+    lin = block.BlockLinear(w.cuda())
+    q, s = R.quantize_weight(w)
+    got = R.unpack(lin.q.cpu(), n, k)
+    assert torch.equal(lin.scale.cpu(), s)
+    assert torch.equal(got[:n, :k].view(torch.float8_e4m3fn).double(), q)
+    assert (got[n:] == 0).all()
+    turned = block.BlockLinear(w.T.contiguous().cuda().T)      # columns contiguous
+    assert torch.equal(turned.q, lin.q)
+
+
+SHAPES = [
+    # rows, n, k
+    (1, 1, 1), (1, 16, 128), (1, 333, 700), (2, 4, 8192), (5, 130, 96), (15, 64, 512), (16, 48, 1030), (17, 129, 256),
+    (33, 257, 384), (48, 100, 1280), (63, 1024, 128), (64, 272, 2176), (65, 96, 640), (100, 515, 300),
+    (129, 256, 1024), (200, 1000, 136), (255, 384, 512), (257, 513, 260), (300, 128, 4096), (513, 640, 384),
+    (1000, 260, 129), (1030, 2050, 256), (2000, 1, 500), (1, 5000, 128),
+]
+
+
+@pytest.mark.parametrize("act,out", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("rows,n,k", SHAPES)
+def test_product(act, out, rows, n, k):
+    g = gen(rows * 31 + n * 7 + k)
+    x = rows_of(g, rows, k, act)
+    codes, scale = weight_of(g, n, k)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda(), dtype=act, out_dtype=out)
+    y = lin(x.cuda())
+    assert y.dtype == out
+    check(lin, x, codes.double(), scale, y)
+    # the codes by themselves, and as bytes, give the same bits
+    assert torch.equal(lin(codes=lin.quantize(x.cuda())), y)
+    again = block.BlockLinear(codes.view(torch.uint8).cuda(), scale.cuda(), dtype=act, out_dtype=out)
+    assert torch.equal(again(x.cuda()), y)
+
+
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_rows_are_independent(act):
+    """A row's result does not go by the rows beside it beyond the additions' order, and
+    NaN and infinities stay in their row."""
+    g = gen(5)
+    x = rows_of(g, 300, 384, act)
+    codes, scale = weight_of(g, 200, 384)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda(), dtype=act, out_dtype=F32)
+    y = lin(x.cuda())
+    x[7, 200], x[100, 3], x[299, 383] = math.nan, math.inf, -math.inf
+    z = lin(x.cuda())
+    bad = torch.tensor([7, 100, 299])
+    assert z[bad.cuda()].isnan().all()
+    keep = torch.ones(300, dtype=torch.bool)
+    keep[bad] = False
+    assert torch.equal(z[keep.cuda()], y[keep.cuda()])
+
+
+def test_weights_that_are_not_finite():
+    g = gen(6)
+    x = rows_of(g, 20, 256, BF16)
+    w = torch.randn(300, 256, generator=g)
+    w[130, 5] = math.inf
+    y = block.BlockLinear(w.cuda(), out_dtype=F32)(x.cuda())
+    assert y[:, 128:256].isnan().all() and y[:, :128].isfinite().all() and y[:, 256:].isfinite().all()
+
+
+@pytest.mark.parametrize("rows", [3, 70, 400])
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_strided_and_unaligned_rows(rows, act):
+    g = gen(rows)
+    wide = rows_of(g, rows, 700, act).cuda()
+    codes, scale = weight_of(g, 150, 260)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda(), dtype=act, out_dtype=F32)
+    for at in (0, 1, 8, 440):
+        x = wide[:, at:at + 260]
+        assert torch.equal(lin(x), lin(x.contiguous()))
+    same = wide[:1, :260].expand(rows, 260)                    # a stride of zero
+    assert torch.equal(lin(same), lin(same.contiguous()))
+
+
+def test_no_rows_and_large_and_small_values():
+    codes, scale = weight_of(gen(1), 40, 256)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda())
+    assert lin(torch.empty(0, 256, dtype=BF16, device="cuda")).shape == (0, 40)
+    c = lin.quantize(torch.empty(0, 256, dtype=BF16, device="cuda"))
+    assert lin(codes=c).shape == (0, 40)
+    x = torch.randn(6, 256, generator=gen(2))
+    x = x * torch.tensor([1e30, 1e-30, 3e-38, 1e-44, 0.0, 1.0])[:, None]
+    f32 = block.BlockLinear(codes.cuda(), scale.cuda(), dtype=F32)
+    y = f32(x.cuda())
+    check(f32, x, codes.double(), scale, y)
+    assert (y[4] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 64, 300])
+def test_captured_and_on_another_stream(rows):
+    g = gen(rows)
+    codes, scale = weight_of(g, 272, 640)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda())
+    xs = [rows_of(g, rows, 640, BF16).cuda() for _ in range(3)]
+    want = [lin(x).clone() for x in xs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = lin(xs[0], stream=side)
+    side.synchronize()
+    assert torch.equal(got, want[0])
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = lin(x)
+    for a, b in list(zip(xs, want)) * 2:
+        x.copy_(a)
+        graph.replay()
+        lin(xs[1])
+        torch.cuda.synchronize()
+        assert torch.equal(y, b)
+
+
+def test_refuses():
+    w = torch.randn(40, 256, device="cuda")
+    codes, scale = (t.cuda() for t in weight_of(gen(1), 40, 256))
+    for bad in (dict(weight=w, scale=scale), dict(weight=codes), dict(weight=codes, scale=scale[:, :1]),
+                dict(weight=codes, scale=scale.double()), dict(weight=w.half()), dict(weight=w[0]),
+                dict(weight=w, dtype=torch.float16), dict(weight=w, out_dtype=torch.float64), dict(weight=w.cpu()),
+                dict(weight=codes, scale=scale.cpu()), dict(weight=w[:0])):
+        with pytest.raises(ValueError):
+            block.BlockLinear(**bad)
+    lin = block.BlockLinear(w)
+    x = torch.randn(3, 256, device="cuda").to(BF16)
+    for bad in (x.float(), x[:, :255], x[0], x.cpu(), x.T):
+        with pytest.raises(ValueError):
+            lin(bad)
+    with pytest.raises(ValueError):
+        lin()
+    c = lin.quantize(x)
+    with pytest.raises(ValueError):
+        lin(x, codes=c)
+    other = block.BlockLinear(torch.randn(40, 300, device="cuda"))
+    with pytest.raises(ValueError):
+        other(codes=c)
+    with pytest.raises(ValueError):
+        lin(codes=c._replace(rows=17))
+    with pytest.raises(AttributeError):
+        lin.q = codes
