@@ -46,10 +46,11 @@ __device__ __forceinline__ f32x4 block_product(const i32x4 &w0, const i32x4 &w1,
 
 // ----------------------------------------------------------------------------- codes
 
-// Scale of a block with the largest magnitude am: am / 448 in fp32, 0 for zeros, at
-// least the smallest normal number otherwise; NaN for an infinity or NaN.
+// Scale of a block with the largest magnitude am: am times the fp32 number 1/448, rounded
+// to fp32, 0 for zeros, at least the smallest normal number otherwise; NaN for an infinity
+// or NaN.
 __device__ __forceinline__ float block_scale(float am) {
-  return am > 0.0f && am < INFINITY ? fmaxf(am / 448.0f, 0x1p-126f) : am == 0.0f ? 0.0f : __builtin_nanf("");
+  return am > 0.0f && am < INFINITY ? fmaxf(am * (1.0f / 448.0f), 0x1p-126f) : am == 0.0f ? 0.0f : __builtin_nanf("");
 }
 // E4M3 code of v / scale: the quotient in 64 bits (a multiplication by the inverse and a
 // correction, which makes quotients that 64 bits hold exact), then to the code by way of

@@ -25,7 +25,7 @@ def e4m3_nearest(v):
 
 def scale_of(top):
     """fp32 scale of blocks with the largest magnitudes `top` (any float type)."""
-    s = (top.float() / 448.0).clamp(min=2.0 ** -126)
+    s = (top.float() * torch.tensor(1.0 / 448.0)).clamp(min=2.0 ** -126)
     s = torch.where(top.float() == 0, torch.zeros_like(s), s)
     return torch.where(top.isfinite(), s, torch.full_like(s, math.nan))
 

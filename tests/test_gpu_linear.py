@@ -60,7 +60,7 @@ def test_codes_next_to_borders():
     inverse is not exact: a border itself goes to the even code."""
     xs = []
     for top in (140.0, 1.09375, 448.0, 7.0 / 3, 3.3e-5, 133.0):
-        s = float(torch.tensor(top) / 448.0)
+        s = float(R.scale_of(torch.tensor(top)))
         row = [top]
         for m in range(17, 32, 2):               # borders between codes of 4 bits
             for e in (-3, 0, 3):
