@@ -308,7 +308,7 @@ moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, 
   if (!wq || !al(wq, 16) || !w_scale || !al(w_scale, 4) || !out || !al(out, 16) || !al(xq, 16) || !al(xq_scale, 16) ||
       !al(ws, 16))
     return MOE_ERR_INVALID_ARG;
-  if (!linear_fits(rows, n, k)) return MOE_ERR_UNSUPPORTED;
+  if (!linear_fits(rows, n)) return MOE_ERR_UNSUPPORTED;
   if (!xq) {
     if (!x || !al(x, x_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
     if (!ws || ws_bytes < moe_block_linear_workspace_bytes(rows, n, k)) return MOE_ERR_WORKSPACE;

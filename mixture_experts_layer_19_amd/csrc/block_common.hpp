@@ -3,6 +3,7 @@
 #pragma once
 #include "block_launch.hpp"
 #include "moe_common.hpp"
+#include "once_per_device.hpp"
 
 namespace moe {
 
@@ -51,6 +52,16 @@ __device__ __forceinline__ uint2 e4m3_to_bf16x4(uint32_t codes, uint32_t sb) {
   return make_uint2(
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true)));
+}
+
+// Allow `bytes` of dynamic LDS to a kernel on the current device; `once`: of that kernel.
+inline hipError_t allow_lds(OncePerDevice &once, const void *kernel, int bytes) {
+  int device = 0;
+  const hipError_t err = hipGetDevice(&device);
+  if (err != hipSuccess) return err;
+  return (hipError_t)once(device, [&] {
+    return (int)hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
 }
 
 // Eight consecutive elements of a row, 16-byte aligned.

@@ -95,7 +95,7 @@ hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, i
 // src: FMT_F32, FMT_BF16 (scales are written) or FMT_FP8 (codes, which only change places).
 hipError_t launch_block_pack(const void *w, long long stride, int src, int n, int cols, uint8_t *q, float *scale,
                              hipStream_t stream);
-bool linear_fits(int rows, int n, int k);        // within one launch's workgroups
+bool linear_fits(int rows, int n);        // within one launch's workgroups
 hipError_t launch_linear(const LinearArgs &a, int f32_out, hipStream_t stream);
 
 // Token log probabilities (logprobs.hip).

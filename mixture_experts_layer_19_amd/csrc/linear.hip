@@ -192,9 +192,8 @@ template <bool F32, int RT>
 __global__ __launch_bounds__(256) void block_rows_kernel(LinearArgs a) {
   __shared__ f32x4 part[4][RT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = (a.k + kBlk - 1) / kBlk, rows16 = (a.rows + 15) / 16 * 16, n16 = (a.n + 15) / 16;
-  const int nb = blockIdx.x % n16;
-  const int rb0 = blockIdx.x / n16 * RT;
+  const int blocks = (a.k + kBlk - 1) / kBlk, rows16 = (a.rows + 15) / 16 * 16;
+  const int nb = blockIdx.x;
   const int b0 = (int)((long long)blocks * wave / 4), b1 = (int)((long long)blocks * (wave + 1) / 4);
   const uint8_t *w = a.w + (long long)nb * blocks * kBlkBytes + lane * 16;
   const float *ws = a.w_scale + (long long)(nb / 8) * blocks;
@@ -208,7 +207,7 @@ __global__ __launch_bounds__(256) void block_rows_kernel(LinearArgs a) {
     const float sw = ws[b];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int rb = min(rb0 + t, rows16 / 16 - 1);
+      const int rb = min(t, rows16 / 16 - 1);
       const uint8_t *x = a.q + ((long long)rb * blocks + b) * kBlkBytes + lane * 16;
       const f32x4 p = block_product<F32>(w0, w1, *(const i32x4 *)x, *(const i32x4 *)(x + 1024));
       const float s = a.q_scale[(long long)b * rows16 + rb * 16 + (lane & 15)] * sw;
@@ -221,27 +220,153 @@ __global__ __launch_bounds__(256) void block_rows_kernel(LinearArgs a) {
   __syncthreads();
   for (int t = wave; t < RT; t += 4) {
     const f32x4 y = ((part[0][t][lane] + part[1][t][lane]) + part[2][t][lane]) + part[3][t][lane];
-    const long long r = (long long)(rb0 + t) * 16 + (lane & 15);
+    const long long r = (long long)t * 16 + (lane & 15);
     if (r < a.rows) store4<F32>(a, r, nb * 16 + 4 * (lane >> 4), y);
+  }
+}
+
+// Many rows: a tile of TM rows x TN columns a workgroup, WM x WN of it a wave.  Both
+// sides' blocks of 128 columns go from memory to the LDS without passing registers, as
+// they lie (a wave's read of a fragment is 1 KiB in a row), the next one's while this
+// one's products run.
+template <int TM, int TN, int WM, int WN>
+struct TileCfg {
+  static constexpr int waves_n = TN / WN, waves = TM / WM * waves_n, threads = 64 * waves;
+  static constexpr int x_blocks = TM / 16, w_blocks = TN / 16, blocks = x_blocks + w_blocks;
+  static constexpr int stage = blocks * kBlkBytes + TM * 4;      // and the rows' scales
+  static constexpr int lds = 2 * stage;
+  static_assert(blocks % waves == 0 && TM % 64 == 0);
+};
+
+// 16 bytes a lane from base + offset to the LDS at `to` + 16 lane, and the same 1 KiB on.
+__device__ __forceinline__ void block_to_lds(uint32_t to, const uint8_t *base, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\t"
+               "global_load_lds_dwordx4 %1, %2\n\t"
+               "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void word_to_lds(uint32_t to, const void *base, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
+}
+
+template <bool F32, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kernel(LinearArgs a, int tiles_m, int tiles_n) {
+  using C = TileCfg<TM, TN, WM, WN>;
+  constexpr int MT = WM / 16, NT = WN / 16, PER = C::blocks / C::waves, GROUP = 4;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t *)lds;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::waves_n, wn = wave % C::waves_n;
+  const int blocks = (a.k + kBlk - 1) / kBlk, x16 = (a.rows + 15) / 16, n16 = (a.n + 15) / 16;
+
+  // Workgroups go round the eight XCDs; each takes a run of tiles, GROUP row tiles by
+  // all column tiles at a time, so that those that run together share its L2.
+  const int total = tiles_m * tiles_n, per = (total + 7) / 8, tile = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (tile >= total) return;
+  const int first = tile / (GROUP * tiles_n) * GROUP, group = min(GROUP, tiles_m - first), in = tile - first * tiles_n;
+  const int tm = first + in % group, tn = in / group;
+
+  // this wave's blocks of a stage, rows of the tile before columns
+  const uint8_t *src[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int blk = wave * PER + i;
+    src[i] = blk < C::x_blocks ? a.q + (long long)min(tm * C::x_blocks + blk, x16 - 1) * blocks * kBlkBytes
+                               : a.w + (long long)min(tn * C::w_blocks + blk - C::x_blocks, n16 - 1) * blocks * kBlkBytes;
+  }
+  const float *row_scale = a.q_scale + tm * TM;
+  const uint32_t s_off = (min(tm * TM + wave * 64 + lane, x16 * 16 - 1) - tm * TM) * 4;
+  const float *col_scale = a.w_scale + (long long)min((tn * TN + wn * WN) / 128, (n16 - 1) / 8) * blocks;
+  auto load = [&](int b) MOE_INLINE {
+    const uint32_t to = lds0 + (b & 1) * C::stage;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      block_to_lds(to + (wave * PER + i) * kBlkBytes, src[i] + (long long)b * kBlkBytes, lane * 16);
+    if (wave < TM / 64)
+      word_to_lds(to + C::blocks * kBlkBytes + wave * 256, row_scale + (long long)b * x16 * 16, s_off);
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  load(0);
+  float sw = col_scale[0];
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("" : "+v"(sw));
+  for (int b = 0; b < blocks; ++b) {
+    float sw_next = sw;
+    if (b + 1 < blocks) {
+      sw_next = col_scale[b + 1];
+      load(b + 1);
+    }
+    const uint8_t *st = lds + (b & 1) * C::stage + lane * 16;
+    const float *sc = (const float *)(lds + (b & 1) * C::stage + C::blocks * kBlkBytes) + wm * WM + (lane & 15);
+    i32x4 w0[NT], w1[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint8_t *p = st + (C::x_blocks + wn * NT + j) * kBlkBytes;
+      w0[j] = *(const i32x4 *)p;
+      w1[j] = *(const i32x4 *)(p + 1024);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint8_t *p = st + (wm * MT + t) * kBlkBytes;
+      const i32x4 x0 = *(const i32x4 *)p, x1 = *(const i32x4 *)(p + 1024);
+      const float s = sc[16 * t] * sw;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 y = block_product<F32>(w0[j], w1[j], x0, x1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(y[i], s, acc[t][j][i]);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("" : "+v"(sw_next));
+    sw = sw_next;
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const long long r = (long long)tm * TM + wm * WM + t * 16 + (lane & 15);
+    if (r < a.rows)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) store4<F32>(a, r, tn * TN + wn * WN + j * 16 + 4 * (lane >> 4), acc[t][j]);
   }
 }
 
 // ----------------------------------------------------------------------------- launches
 
 namespace {
+template <bool F32, int TM, int TN, int WM, int WN>
+hipError_t tiles(const LinearArgs &a, hipStream_t s) {
+  using C = TileCfg<TM, TN, WM, WN>;
+  static OncePerDevice once;
+  const auto kernel = block_tile_kernel<F32, TM, TN, WM, WN>;
+  const hipError_t err = allow_lds(once, (const void *)kernel, C::lds);
+  if (err != hipSuccess) return err;
+  const int tm = (a.rows + TM - 1) / TM, tn = (a.n + TN - 1) / TN;
+  kernel<<<(unsigned)(((long long)tm * tn + 7) / 8 * 8), C::threads, C::lds, s>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
 template <bool F32>
 hipError_t linear(const LinearArgs &a, hipStream_t s) {
   const int n16 = (a.n + 15) / 16, rb = (a.rows + 15) / 16;
+  if (a.rows > 64) {
+    const long long big = ((a.rows + 255ll) / 256) * ((a.n + 255ll) / 256);
+    return big >= 256 ? tiles<F32, 256, 256, 128, 64>(a, s) : tiles<F32, 128, 128, 64, 64>(a, s);
+  }
   if (rb <= 1) block_rows_kernel<F32, 1><<<n16, 256, 0, s>>>(a);
   else if (rb <= 2) block_rows_kernel<F32, 2><<<n16, 256, 0, s>>>(a);
-  else block_rows_kernel<F32, 4><<<(unsigned)n16 * ((rb + 3) / 4), 256, 0, s>>>(a);
+  else block_rows_kernel<F32, 4><<<n16, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 }  // namespace
 
-bool linear_fits(int rows, int n, int k) {
-  const long long blocks = (k + (kBlk - 1ll)) / kBlk, rb = (rows + 15ll) / 16, n16 = (n + 15ll) / 16;
-  return n16 * ((rb + 3) / 4) <= max_groups(256);
+bool linear_fits(int rows, int n) {
+  const long long n16 = (n + 15ll) / 16, tiles = ((rows + 127ll) / 128) * ((n + 127ll) / 128);
+  return rows <= 64 ? n16 <= max_groups(256) : tiles + 8 <= max_groups(512);
 }
 
 hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, int rows, int cols, uint8_t *q,
