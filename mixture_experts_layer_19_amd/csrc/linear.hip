@@ -26,22 +26,22 @@ constexpr int kBlkBytes = 16 * kBlk;             // 16 rows of it
 // rounded to bf16.  Where it is not, the codes go to bf16, which holds them exactly, and
 // through instructions of half the rate that add in fp32.
 template <bool F32>
-__device__ __forceinline__ f32x4 block_product(const i32x4 &w0, const i32x4 &w1, const i32x4 &x0, const i32x4 &x1) {
+__device__ __forceinline__ f32x4 block_product(const i32x8 &w, const i32x8 &x) {
   f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (!F32) {
-    const i32x8 w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-    const i32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, y, 0, 0, 0, 0, 0, 0);      // no scales
-  }
+  if constexpr (!F32) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, y, 0, 0, 0, 0, 0, 0);    // no scales
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    auto bf16 = [&](const i32x4 &c) MOE_INLINE {
-      const uint2 a = e4m3_to_bf16x4((uint32_t)c[2 * (i & 1)], 127), b = e4m3_to_bf16x4((uint32_t)c[2 * (i & 1) + 1], 127);
+    auto bf16 = [&](const i32x8 &c) MOE_INLINE {
+      const uint2 a = e4m3_to_bf16x4((uint32_t)c[2 * i], 127), b = e4m3_to_bf16x4((uint32_t)c[2 * i + 1], 127);
       return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
     };
-    y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16(i < 2 ? w0 : w1), bf16(i < 2 ? x0 : x1), y, 0, 0, 0);
+    y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16(w), bf16(x), y, 0, 0, 0);
   }
   return y;
+}
+// A lane's 32 bytes of a block at p (its own 16 of the first half)
+__device__ __forceinline__ i32x8 fragment(const uint8_t *p) {
+  return __builtin_shufflevector(*(const i32x4 *)p, *(const i32x4 *)(p + 1024), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // ----------------------------------------------------------------------------- codes
@@ -186,42 +186,92 @@ __device__ __forceinline__ void store4(const LinearArgs &a, long long r, int n, 
   }
 }
 
-// Few rows: 16 RT rows and 16 columns a workgroup, its four waves a quarter of the
-// blocks each, their sums added in the waves' order.
-template <bool F32, int RT>
-__global__ __launch_bounds__(256) void block_rows_kernel(LinearArgs a) {
-  __shared__ f32x4 part[4][RT][64];
+// Few rows: 16 RT rows and 16 CT columns a workgroup, its KW waves a share of the
+// blocks each, their sums added in the waves' order.  The next block's codes are on their
+// way while one's products run.
+template <bool F32, int RT, int CT, int KW>
+__global__ __launch_bounds__(64 * KW) void block_rows_kernel(LinearArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  f32x4 (*part)[RT * CT][64] = (f32x4 (*)[RT * CT][64])lds;      // [KW]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = (a.k + kBlk - 1) / kBlk, rows16 = (a.rows + 15) / 16 * 16;
-  const int nb = blockIdx.x;
-  const int b0 = (int)((long long)blocks * wave / 4), b1 = (int)((long long)blocks * (wave + 1) / 4);
-  const uint8_t *w = a.w + (long long)nb * blocks * kBlkBytes + lane * 16;
-  const float *ws = a.w_scale + (long long)(nb / 8) * blocks;
-  f32x4 acc[RT];
+  const int blocks = (a.k + kBlk - 1) / kBlk, x16 = (a.rows + 15) / 16, n16 = (a.n + 15) / 16;
+  const int nb = blockIdx.x * CT;
+  const int b0 = (int)((long long)blocks * wave / KW), b1 = (int)((long long)blocks * (wave + 1) / KW);
+  const uint8_t *w[CT], *x[RT];
+  const float *ws[CT], *xs[RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int b = b0; b < b1; ++b) {
-    const i32x4 w0 = *(const i32x4 *)(w + (long long)b * kBlkBytes);
-    const i32x4 w1 = *(const i32x4 *)(w + (long long)b * kBlkBytes + 1024);
-    const float sw = ws[b];
+  for (int j = 0; j < CT; ++j) {
+    const int n = min(nb + j, n16 - 1);
+    w[j] = a.w + (long long)n * blocks * kBlkBytes;
+    ws[j] = a.w_scale + (long long)(n / 8) * blocks;
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = min(t, x16 - 1);
+    x[t] = a.q + (long long)r * blocks * kBlkBytes;
+    xs[t] = a.q_scale + r * 16;
+  }
+  struct Block {
+    i32x8 w[CT], x[RT];
+    float ws[CT], xs[RT];
+  };
+  auto read = [&](int b, Block &o) MOE_INLINE {
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      o.w[j] = fragment(w[j] + (long long)b * kBlkBytes + lane * 16);
+      o.ws[j] = ws[j][b];
+    }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int rb = min(t, rows16 / 16 - 1);
-      const uint8_t *x = a.q + ((long long)rb * blocks + b) * kBlkBytes + lane * 16;
-      const f32x4 p = block_product<F32>(w0, w1, *(const i32x4 *)x, *(const i32x4 *)(x + 1024));
-      const float s = a.q_scale[(long long)b * rows16 + rb * 16 + (lane & 15)] * sw;
+      o.x[t] = fragment(x[t] + (long long)b * kBlkBytes + lane * 16);
+      o.xs[t] = xs[t][(long long)b * x16 * 16 + (lane & 15)];
+    }
+  };
+  f32x4 acc[RT][CT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], s, acc[t][i]);
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Block &o) MOE_INLINE {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) {
+        const f32x4 p = block_product<F32>(o.w[j], o.x[t]);
+        const float s = o.xs[t] * o.ws[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(p[i], s, acc[t][j][i]);
+      }
+  };
+  if (b0 < b1) {
+    Block one, two;
+    read(b0, one);
+    int b = b0;
+    for (; b + 2 < b1; b += 2) {
+      read(b + 1, two);
+      multiply(one);
+      read(b + 2, one);
+      multiply(two);
+    }
+    if (b + 1 < b1) {
+      read(b + 1, two);
+      multiply(one);
+      multiply(two);
+    } else {
+      multiply(one);
     }
   }
 #pragma unroll
-  for (int t = 0; t < RT; ++t) part[wave][t][lane] = acc[t];
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) part[wave][t * CT + j][lane] = acc[t][j];
   __syncthreads();
-  for (int t = wave; t < RT; t += 4) {
-    const f32x4 y = ((part[0][t][lane] + part[1][t][lane]) + part[2][t][lane]) + part[3][t][lane];
-    const long long r = (long long)t * 16 + (lane & 15);
-    if (r < a.rows) store4<F32>(a, r, nb * 16 + 4 * (lane >> 4), y);
+  for (int i = wave; i < RT * CT; i += KW) {
+    f32x4 y = part[0][i][lane];
+#pragma unroll
+    for (int v = 1; v < KW; ++v) y += part[v][i][lane];
+    const long long r = (long long)(i / CT) * 16 + (lane & 15);
+    if (r < a.rows) store4<F32>(a, r, (nb + i % CT) * 16 + 4 * (lane >> 4), y);
   }
 }
 
@@ -274,58 +324,101 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
                                : a.w + (long long)min(tn * C::w_blocks + blk - C::x_blocks, n16 - 1) * blocks * kBlkBytes;
   }
   const float *row_scale = a.q_scale + tm * TM;
-  const uint32_t s_off = (min(tm * TM + wave * 64 + lane, x16 * 16 - 1) - tm * TM) * 4;
+  const int s64 = wave % (TM / 64) * 64;         // (more waves than that load the same ones)
+  const uint32_t s_off = (min(tm * TM + s64 + lane, x16 * 16 - 1) - tm * TM) * 4;
   const float *col_scale = a.w_scale + (long long)min((tn * TN + wn * WN) / 128, (n16 - 1) / 8) * blocks;
   auto load = [&](int b) MOE_INLINE {
     const uint32_t to = lds0 + (b & 1) * C::stage;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       block_to_lds(to + (wave * PER + i) * kBlkBytes, src[i] + (long long)b * kBlkBytes, lane * 16);
-    if (wave < TM / 64)
-      word_to_lds(to + C::blocks * kBlkBytes + wave * 256, row_scale + (long long)b * x16 * 16, s_off);
+    word_to_lds(to + C::blocks * kBlkBytes + s64 * 4, row_scale + (long long)b * x16 * 16, s_off);
   };
 
-  f32x4 acc[MT][NT];
+  // Fragments are read one row tile ahead, and a tile's products are added under the
+  // next one's: in this order, which the compiler's own is slower than.  Before the last
+  // row tile of a block everything of it is in registers: there all waves meet, the
+  // block after the next starts into its place, and the next one's first fragments are
+  // read under the last tile's products.
+  f32x4 acc[MT][NT], y[2][NT];
+  i32x8 wf[NT], xf[2];
+  float rs[2], f = 0.0f;                         // f: of the tile whose products are added
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int j = 0; j < NT; ++j) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    y[1][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  auto read_x = [&](int b, int t) MOE_INLINE {
+    const uint8_t *st = lds + (b & 1) * C::stage;
+    xf[t & 1] = fragment(st + (wm * MT + t) * kBlkBytes + lane * 16);
+    rs[t & 1] = ((const float *)(st + C::blocks * kBlkBytes))[wm * WM + 16 * t + (lane & 15)];
+  };
+  auto read_w = [&](int b, int j) MOE_INLINE {
+    wf[j] = fragment(lds + (b & 1) * C::stage + (C::x_blocks + wn * NT + j) * kBlkBytes + lane * 16);
+  };
+  auto add_up = [&](int t, int j) MOE_INLINE {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(y[t & 1][j][i], f, acc[t][j][i]);
+  };
 
   load(0);
-  float sw = col_scale[0];
+  float sw = col_scale[0], sw_next = sw;
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  asm volatile("" : "+v"(sw));
-  for (int b = 0; b < blocks; ++b) {
-    float sw_next = sw;
-    if (b + 1 < blocks) {
-      sw_next = col_scale[b + 1];
-      load(b + 1);
-    }
-    const uint8_t *st = lds + (b & 1) * C::stage + lane * 16;
-    const float *sc = (const float *)(lds + (b & 1) * C::stage + C::blocks * kBlkBytes) + wm * WM + (lane & 15);
-    i32x4 w0[NT], w1[NT];
+  if (blocks > 1) {
+    sw_next = col_scale[1];
+    load(1);
+  }
+  read_x(0, 0);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint8_t *p = st + (C::x_blocks + wn * NT + j) * kBlkBytes;
-      w0[j] = *(const i32x4 *)p;
-      w1[j] = *(const i32x4 *)(p + 1024);
-    }
+  for (int j = 0; j < NT; ++j) read_w(0, j);
+  auto block = [&](int b, auto left) MOE_INLINE {
+    constexpr bool MORE = decltype(left)::value > 0;       // another block behind it, and one more
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const uint8_t *p = st + (wm * MT + t) * kBlkBytes;
-      const i32x4 x0 = *(const i32x4 *)p, x1 = *(const i32x4 *)(p + 1024);
-      const float s = sc[16 * t] * sw;
+      const float own = sw;
+      if (t + 1 < MT) {
+        read_x(b, t + 1);
+      } else if constexpr (MORE) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("" : "+v"(sw_next));
+        sw = sw_next;
+        if constexpr (decltype(left)::value > 1) {
+          sw_next = col_scale[b + 2];
+          load(b + 2);
+        }
+        read_x(b + 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const f32x4 y = block_product<F32>(w0[j], w1[j], x0, x1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(y[i], s, acc[t][j][i]);
+        y[t & 1][j] = block_product<F32>(wf[j], xf[t & 1]);
+        if (MORE && t + 1 == MT) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_w(b + 1, j);
+        }
+        add_up(t > 0 ? t - 1 : MT - 1, j);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      f = rs[t & 1] * own;
+      __builtin_amdgcn_sched_barrier(0);
     }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    asm volatile("" : "+v"(sw_next));
-    sw = sw_next;
-  }
+    // (or the compiler carries additions past the end of a block, in more registers
+    // than there are)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        f32x4 &sum = acc[t][j];
+        asm volatile("" : "+v"(sum));
+      }
+  };
+  for (int b = 0; b + 2 < blocks; ++b) block(b, std::integral_constant<int, 2>{});
+  if (blocks > 1) block(blocks - 2, std::integral_constant<int, 1>{});
+  block(blocks - 1, std::integral_constant<int, 0>{});
+#pragma unroll
+  for (int j = 0; j < NT; ++j) add_up(MT - 1, j);
+  // the tile's rows out
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const long long r = (long long)tm * TM + wm * WM + t * 16 + (lane & 15);
@@ -350,17 +443,42 @@ hipError_t tiles(const LinearArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool F32, int RT, int CT, int KW>
+hipError_t few(const LinearArgs &a, hipStream_t s) {
+  constexpr int lds = KW * RT * CT * 1024;
+  static OncePerDevice once;
+  const hipError_t err = allow_lds(once, (const void *)block_rows_kernel<F32, RT, CT, KW>, lds);
+  if (err != hipSuccess) return err;
+  block_rows_kernel<F32, RT, CT, KW><<<(unsigned)((a.n + 16ll * CT - 1) / (16 * CT)), 64 * KW, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+// Blocks of 16 columns of a workgroup, of few rows: as many as leave the fullest of the
+// 256 CUs no more of them.
+int columns_of_group(int blocks) {
+  int best = 1, most = 1 << 30;
+  for (int ct = 1; ct <= 3; ++ct) {
+    const int groups = (blocks + ct - 1) / ct, load = (groups + 255) / 256 * ct;
+    if (load <= most) most = load, best = ct;
+  }
+  return best;
+}
+
+template <bool F32, int RT>
+hipError_t few(const LinearArgs &a, hipStream_t s) {
+  const int ct = columns_of_group((a.n + 15) / 16);
+  return ct == 3 ? few<F32, RT, 3, 4>(a, s) : ct == 2 ? few<F32, RT, 2, 4>(a, s)
+         : RT == 1 ? few<F32, RT, 1, 4>(a, s) : few<F32, RT, 1, 8>(a, s);
+}
+
 template <bool F32>
 hipError_t linear(const LinearArgs &a, hipStream_t s) {
-  const int n16 = (a.n + 15) / 16, rb = (a.rows + 15) / 16;
   if (a.rows > 64) {
     const long long big = ((a.rows + 255ll) / 256) * ((a.n + 255ll) / 256);
     return big >= 256 ? tiles<F32, 256, 256, 128, 64>(a, s) : tiles<F32, 128, 128, 64, 64>(a, s);
   }
-  if (rb <= 1) block_rows_kernel<F32, 1><<<n16, 256, 0, s>>>(a);
-  else if (rb <= 2) block_rows_kernel<F32, 2><<<n16, 256, 0, s>>>(a);
-  else block_rows_kernel<F32, 4><<<n16, 256, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.rows > 32 && a.n >= 32768) return tiles<F32, 64, 64, 64, 32>(a, s);
+  return a.rows <= 16 ? few<F32, 1>(a, s) : a.rows <= 32 ? few<F32, 2>(a, s) : few<F32, 4>(a, s);
 }
 }  // namespace
 
