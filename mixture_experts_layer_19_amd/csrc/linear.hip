@@ -283,9 +283,10 @@ template <int TM, int TN, int WM, int WN>
 struct TileCfg {
   static constexpr int waves_n = TN / WN, waves = TM / WM * waves_n, threads = 64 * waves;
   static constexpr int x_blocks = TM / 16, w_blocks = TN / 16, blocks = x_blocks + w_blocks;
-  static constexpr int stage = blocks * kBlkBytes + TM * 4;      // and the rows' scales
+  static constexpr int scales = (TM + 63) / 64;                  // of 64 rows
+  static constexpr int stage = blocks * kBlkBytes + scales * 256;
   static constexpr int lds = 2 * stage;
-  static_assert(blocks % waves == 0 && TM % 64 == 0);
+  static_assert(WM % 32 == 0, "fragments take turns");
 };
 
 // 16 bytes a lane from base + offset to the LDS at `to` + 16 lane, and the same 1 KiB on.
@@ -301,7 +302,7 @@ __device__ __forceinline__ void word_to_lds(uint32_t to, const void *base, uint3
 template <bool F32, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kernel(LinearArgs a, int tiles_m, int tiles_n) {
   using C = TileCfg<TM, TN, WM, WN>;
-  constexpr int MT = WM / 16, NT = WN / 16, PER = C::blocks / C::waves, GROUP = 4;
+  constexpr int MT = WM / 16, NT = WN / 16, PER = (C::blocks + C::waves - 1) / C::waves, GROUP = 4;
   extern __shared__ __align__(16) uint8_t lds[];
   const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t *)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -319,19 +320,19 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
   const uint8_t *src[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int blk = wave * PER + i;
+    const int blk = min(wave * PER + i, C::blocks - 1);          // (the last one may be loaded twice)
     src[i] = blk < C::x_blocks ? a.q + (long long)min(tm * C::x_blocks + blk, x16 - 1) * blocks * kBlkBytes
                                : a.w + (long long)min(tn * C::w_blocks + blk - C::x_blocks, n16 - 1) * blocks * kBlkBytes;
   }
   const float *row_scale = a.q_scale + tm * TM;
-  const int s64 = wave % (TM / 64) * 64;         // (more waves than that load the same ones)
+  const int s64 = wave % C::scales * 64;         // (more waves than that load the same ones)
   const uint32_t s_off = (min(tm * TM + s64 + lane, x16 * 16 - 1) - tm * TM) * 4;
   const float *col_scale = a.w_scale + (long long)min((tn * TN + wn * WN) / 128, (n16 - 1) / 8) * blocks;
   auto load = [&](int b) MOE_INLINE {
     const uint32_t to = lds0 + (b & 1) * C::stage;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      block_to_lds(to + (wave * PER + i) * kBlkBytes, src[i] + (long long)b * kBlkBytes, lane * 16);
+      block_to_lds(to + min(wave * PER + i, C::blocks - 1) * kBlkBytes, src[i] + (long long)b * kBlkBytes, lane * 16);
     word_to_lds(to + C::blocks * kBlkBytes + s64 * 4, row_scale + (long long)b * x16 * 16, s_off);
   };
 
@@ -419,6 +420,32 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
 #pragma unroll
   for (int j = 0; j < NT; ++j) add_up(MT - 1, j);
   // the tile's rows out
+  if (!F32 && a.n % 8 == 0) {
+    // By way of the LDS, a wave's rows by themselves, so that a store is 16 bytes a lane
+    // and whole lines: 16-byte pieces of a row lie turned by the row, which spreads the
+    // banks.
+    constexpr int PIECES = WN / 8;
+    static_assert(C::waves * WM * WN * 2 <= C::lds, "the waves' rows");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    uint8_t *own = lds + wave * WM * WN * 2;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int r = t * 16 + (lane & 15), piece = (2 * j + (lane >> 5)) ^ (r % PIECES);
+        *(uint2 *)(own + (r * PIECES + piece) * 16 + (lane >> 4 & 1) * 8) =
+            make_uint2(bf16_pack2(acc[t][j][0], acc[t][j][1]), bf16_pack2(acc[t][j][2], acc[t][j][3]));
+      }
+    const int piece = lane % PIECES, n = tn * TN + wn * WN + 8 * piece;
+#pragma unroll
+    for (int i = 0; i < WM * PIECES / 64; ++i) {
+      const int r = i * (64 / PIECES) + lane / PIECES;
+      const long long row = (long long)tm * TM + wm * WM + r;
+      const i32x4 v = *(const i32x4 *)(own + (r * PIECES + (piece ^ (r % PIECES))) * 16);
+      if (row < a.rows && n < a.n) *(i32x4 *)((uint16_t *)a.out + row * a.n + n) = v;
+    }
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const long long r = (long long)tm * TM + wm * WM + t * 16 + (lane & 15);
@@ -475,6 +502,9 @@ template <bool F32>
 hipError_t linear(const LinearArgs &a, hipStream_t s) {
   if (a.rows > 64) {
     const long long big = ((a.rows + 255ll) / 256) * ((a.n + 255ll) / 256);
+#ifdef TST
+    return tiles<F32, TST>(a, s);
+#endif
     return big >= 256 ? tiles<F32, 256, 256, 128, 64>(a, s) : tiles<F32, 128, 128, 64, 64>(a, s);
   }
   if (a.rows > 32 && a.n >= 32768) return tiles<F32, 64, 64, 64, 32>(a, s);
