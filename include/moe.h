@@ -506,15 +506,12 @@ MOE_API moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int
  * token outside [0, vocab).  A row of nothing else gives -infinity everywhere
  * and the entropy 0, one with a NaN or +infinity NaN; among the alternatives
  * NaN come last.  tokens: 4 or 8 bytes each (token_bytes).  top: 0 (top_logprob and
- * top_token are not used) to min(vocab, 64).  Sums in fp32.  ws:
- * moe_token_logprobs_workspace_bytes() bytes (0: none needed, or invalid
- * arguments). */
+ * top_token are not used) to min(vocab, 64).  Sums in fp32. */
 #define MOE_LOGPROBS_MAX_TOP 64
-MOE_API size_t moe_token_logprobs_workspace_bytes(int dtype, int32_t rows, int32_t vocab, int32_t top);
 MOE_API moe_status moe_token_logprobs(const void *logits, int dtype, int64_t row_stride, const void *tokens,
                               int32_t token_bytes, int32_t rows, int32_t vocab, int32_t top,
                               float *logprob, float *entropy, float *top_logprob,
-                              int32_t *top_token, void *ws, size_t ws_bytes, void *stream);
+                              int32_t *top_token, void *stream);
 
 #ifdef __cplusplus
 }

@@ -30,7 +30,7 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_status_string", "moe_ctx_la
            "moe_attention", "moe_head_norm_rope", "moe_head_norm_rope_write",
            "moe_block_packed_bytes", "moe_block_quantize", "moe_block_pack",
            "moe_block_linear_workspace_bytes", "moe_block_linear",
-           "moe_token_logprobs_workspace_bytes", "moe_token_logprobs")
+           "moe_token_logprobs")
 MOE_NO_QUANT = -1
 STAGES = ("route", "mx_quant", "permute", "gate_up", "down", "shared_gate_up", "shared_down",
           "combine")
@@ -132,8 +132,7 @@ def lib():
             "moe_block_linear_workspace_bytes": ([I32, I32, I32], S),
             "moe_block_linear": ([P, P, I32, I32, P, ctypes.c_int, I64, P, P, I32, P, ctypes.c_int, P,
                                   S, P], ctypes.c_int),
-            "moe_token_logprobs_workspace_bytes": ([ctypes.c_int, I32, I32, I32], S),
-            "moe_token_logprobs": ([P, ctypes.c_int, I64, P, I32, I32, I32, I32, P, P, P, P, P, S, P],
+            "moe_token_logprobs": ([P, ctypes.c_int, I64, P, I32, I32, I32, I32, P, P, P, P, P],
                                    ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -342,12 +341,8 @@ def moe_block_linear(wq, w_scale, n, k, x, x_dtype, x_stride, xq, xq_scale, rows
                                   _stream(stream)))
 
 
-def moe_token_logprobs_workspace_bytes(dtype: int, rows: int, vocab: int, top: int) -> int:
-    return lib().moe_token_logprobs_workspace_bytes(dtype, rows, vocab, top)
-
-
 def moe_token_logprobs(logits, dtype, row_stride, tokens, token_bytes, rows, vocab, top, logprob, entropy,
-                       top_logprob, top_token, ws, ws_bytes, stream=None):
+                       top_logprob, top_token, stream=None):
     _check(lib().moe_token_logprobs(_ptr(logits), dtype, row_stride, _ptr(tokens), token_bytes, rows, vocab,
                                     top, _ptr(logprob), _ptr(entropy), _ptr(top_logprob), _ptr(top_token),
-                                    _ptr(ws), ws_bytes, _stream(stream)))
+                                    _stream(stream)))

@@ -564,22 +564,17 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, 
     if other is not None:
         with other:
             return token_logprobs(logits, tokens, top)
-    lib, dtype, new = B.lib(), _ACT[logits.dtype], torch.empty_strided
-    logprob = new((rows,), (1,), dtype=torch.float32, device=dev)
-    entropy = new((rows,), (1,), dtype=torch.float32, device=dev)
-    values = ids = ws = None
-    vp = ip = wp = 0
+    new = torch.empty_strided
+    logprob, entropy = new((2, rows), (rows, 1), dtype=torch.float32, device=dev).unbind()
+    values = ids = None
+    vp = ip = 0
     if top:
         values = new((rows, top), (top, 1), dtype=torch.float32, device=dev)
         ids = new((rows, top), (top, 1), dtype=torch.int32, device=dev)
         vp, ip = values.data_ptr(), ids.data_ptr()
-    size = lib.moe_token_logprobs_workspace_bytes(dtype, rows, vocab, top)
-    if size:
-        ws = new((size,), (1,), dtype=torch.uint8, device=dev)
-        wp = ws.data_ptr()
-    rc = lib.moe_token_logprobs(logits.data_ptr(), dtype, logits.stride(0), tokens.data_ptr(), tokens.element_size(),
-                                rows, vocab, top, logprob.data_ptr(), entropy.data_ptr(), vp, ip, wp, size,
-                                _raw_stream(dev.index))
+    rc = B.lib().moe_token_logprobs(logits.data_ptr(), _ACT[logits.dtype], logits.stride(0), tokens.data_ptr(),
+                                    tokens.element_size(), rows, vocab, top, logprob.data_ptr(), entropy.data_ptr(),
+                                    vp, ip, _raw_stream(dev.index))
     if rc:
         B._check(rc)
     return TokenLogprobs(logprob, entropy, values, ids)

@@ -138,11 +138,6 @@ moe_status head_norm_args(const moe_head_norm *n, int heads, const void *q, int6
 bool logprob_args(int dtype, int32_t rows, int32_t vocab, int32_t top) {
   return float_type(dtype) && rows >= 0 && vocab > 0 && top >= 0 && top <= kLogprobTop && top <= vocab;
 }
-size_t logprob_ws(int dtype, int32_t rows, int32_t vocab, int32_t top) {
-  const int parts = logprob_parts(rows, vocab, dtype == MOE_BF16);
-  return parts == 1 ? 0 : (size_t)rows * parts * (16 + 8 * (size_t)top);
-}
-
 size_t workspace(const AttnArgs &a) {
   if (a.c.rows <= 0) return 0;
   return few_rows(a) ? attn_rows_ws_bytes(a) : attn_tile_ws_bytes(a);
@@ -324,25 +319,16 @@ moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, 
   return done(launch_linear(a, out_dtype == MOE_F32, (hipStream_t)stream));
 }
 
-size_t moe_token_logprobs_workspace_bytes(int dtype, int32_t rows, int32_t vocab, int32_t top) {
-  return logprob_args(dtype, rows, vocab, top) ? logprob_ws(dtype, rows, vocab, top) : 0;
-}
-
 moe_status moe_token_logprobs(const void *logits, int dtype, int64_t row_stride, const void *tokens,
                               int32_t token_bytes, int32_t rows, int32_t vocab, int32_t top, float *logprob,
-                              float *entropy, float *top_logprob, int32_t *top_token, void *ws,
-                              size_t ws_bytes, void *stream) {
+                              float *entropy, float *top_logprob, int32_t *top_token, void *stream) {
   if (!logprob_args(dtype, rows, vocab, top) || (token_bytes != 4 && token_bytes != 8)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (!logits || !al(logits, dtype == MOE_F32 ? 4 : 2) || !tokens || !al(tokens, token_bytes)) return MOE_ERR_INVALID_ARG;
   if (!logprob || !al(logprob, 4) || !entropy || !al(entropy, 4)) return MOE_ERR_INVALID_ARG;
   if (top && (!top_logprob || !al(top_logprob, 4) || !top_token || !al(top_token, 4))) return MOE_ERR_INVALID_ARG;
-  if (!al(ws, 16)) return MOE_ERR_INVALID_ARG;
-  const size_t need = logprob_ws(dtype, rows, vocab, top);
-  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   const LogprobArgs a = {logits, row_stride, tokens, dtype == MOE_BF16, token_bytes, rows, vocab, top,
-                         logprob_parts(rows, vocab, dtype == MOE_BF16), logprob, entropy, top_logprob, top_token,
-                         (uint8_t *)ws};
+                         logprob, entropy, top_logprob, top_token};
   return done(launch_logprobs(a, (hipStream_t)stream));
 }
 

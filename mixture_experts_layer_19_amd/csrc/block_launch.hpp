@@ -100,18 +100,15 @@ hipError_t launch_linear(const LinearArgs &a, int f32_out, hipStream_t stream);
 
 // Token log probabilities (logprobs.hip).
 constexpr int kLogprobTop = 64;                  // alternatives at most
-constexpr int kLogprobParts = 32;                // parts of a row at most
 struct LogprobArgs {
   const void *logits;          // [rows][vocab], stride in elements
   long long stride;
   const void *tokens;          // [rows] of token_bytes
-  int is_bf16, token_bytes, rows, vocab, top, parts;
+  int is_bf16, token_bytes, rows, vocab, top;
   float *logprob, *entropy;    // [rows]
   float *top_logprob;          // [rows][top]
   int32_t *top_token;
-  uint8_t *ws;                 // parts > 1: [rows][parts] sums of 16 bytes, then [rows][parts][top] keys of 8
 };
-int logprob_parts(int rows, int vocab, int is_bf16);
 hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t stream);
 
 }  // namespace moe

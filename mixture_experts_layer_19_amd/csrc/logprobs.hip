@@ -15,16 +15,15 @@
 // Elements compare as 64-bit keys, the value's order above the index's complement, so
 // that there are no ties, and the list's own order does not matter.
 //
-// Bound by memory.  Few rows are cut into parts, which a second launch joins.
+// Bound by memory where rows are many; a row by itself is read by one workgroup, which
+// one CU's share of the bandwidth and the steps behind it bound.
 #include "block_common.hpp"
 
 namespace moe {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr int kTop = kLogprobTop;
 constexpr int kList = 512;                       // keys that are ranked by counting
-constexpr int kSweep = 2048;                     // keys that one sweep adds at most
-static_assert(kTop <= 64 && kLogprobParts * kTop <= kSweep, "keys of a list");
+static_assert(kLogprobTop <= 64 && kLogprobTop <= kList, "n-th largest of the maxima");
 
 // Order of a value as an unsigned number: NaN 0, then -infinity upwards; -0 is 0.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -43,13 +42,16 @@ struct Sums {
 // The distance of two maxima in units of log 2, for factors e^: what is infinitely
 // far (or NaN, of two infinities) goes to a finite one with the factor 0.
 __device__ __forceinline__ float apart(float from, float to) { return fmaxf((from - to) * kLog2e, -1.0e4f); }
+// (no fused operations: either order of the two gives the same bits, and so every thread
+// that joins the same sums)
 __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
+#pragma clang fp contract(off)
   Sums r;
   r.m = fmaxf(a.m, b.m);
   const float da = apart(a.m, r.m), db = apart(b.m, r.m);
   const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
   r.l = a.l * fa + b.l * fb;
-  r.t = fmaf(a.l, da, a.t) * fa + fmaf(b.l, db, b.t) * fb;
+  r.t = (a.t + a.l * da) * fa + (b.t + b.l * db) * fb;
   return r;
 }
 template <int N>
@@ -70,31 +72,40 @@ __device__ __forceinline__ void add(Sums &s, const float (&v)[N]) {
     s.t = fmaf(e, fmaxf(d, -200.0f), s.t);       // e is 0 there; 0 x -infinity would be NaN
   }
 }
-// The sums of all 256 threads, in every thread.
+// T threads a row; vectors of E elements.
+template <int T, int E>
+struct __align__(16) LogprobLds {
+  static constexpr int waves = T / 64, keys = kList + T * E, per = (keys + T - 1) / T;
+  static constexpr int groups = T < 256 ? T : 256;         // of threads, whose maxima are ordered
+  uint64_t list[keys];           // what one sweep of all threads may add beyond those that are ranked
+  uint32_t most[groups];         // order of the maximum of each group of threads
+  uint32_t owner[T];
+  Sums red[waves];
+  int owners, count, tally[2];
+  uint32_t least;
+};
+// The sums of all threads, in every thread.
+template <int WAVES>
 __device__ __forceinline__ Sums join_group(Sums s, Sums *red) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1)
     s = join(s, Sums{__shfl_xor(s.m, m, 64), __shfl_xor(s.l, m, 64), __shfl_xor(s.t, m, 64)});
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  return join(join(red[0], red[1]), join(red[2], red[3]));
+  s = red[threadIdx.x % WAVES];
+#pragma unroll
+  for (int m = 1; m < WAVES; m <<= 1)
+    s = join(s, Sums{__shfl_xor(s.m, m, 64), __shfl_xor(s.l, m, 64), __shfl_xor(s.t, m, 64)});
+  return s;
 }
 
-struct __align__(16) LogprobLds {
-  uint64_t list[kList + kSweep];
-  uint32_t most[256];            // order of each thread's maximum
-  Sums red[4];
-  uint32_t owner[256];
-  int owners, count, tally[2];
-  uint32_t least;
-};
-
 // The n-th largest of the list's `count` keys (n <= count; keys differ): bit by bit.
-__device__ __forceinline__ uint64_t nth_largest(LogprobLds &s, int count, int n) {
-  constexpr int PER = (kList + kSweep) / 256;
+template <int T, int E>
+__device__ __forceinline__ uint64_t nth_largest(LogprobLds<T, E> &s, int count, int n) {
+  constexpr int PER = LogprobLds<T, E>::per;
   uint64_t k[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) k[i] = i * 256 + (int)threadIdx.x < count ? s.list[i * 256 + threadIdx.x] : 0;
+  for (int i = 0; i < PER; ++i) k[i] = i * T + (int)threadIdx.x < count ? s.list[i * T + threadIdx.x] : 0;
   uint64_t found = 0;
   if (threadIdx.x < 2) s.tally[threadIdx.x] = 0;
   for (int bit = 63; bit >= 0; --bit) {
@@ -111,12 +122,13 @@ __device__ __forceinline__ uint64_t nth_largest(LogprobLds &s, int count, int n)
   return found;
 }
 // Leave the list's n largest keys in it (n <= count); the smallest of them.
-__device__ __forceinline__ uint64_t prune(LogprobLds &s, int count, int n) {
-  constexpr int PER = (kList + kSweep) / 256;
+template <int T, int E>
+__device__ __forceinline__ uint64_t prune(LogprobLds<T, E> &s, int count, int n) {
+  constexpr int PER = LogprobLds<T, E>::per;
   const uint64_t least = nth_largest(s, count, n);
   uint64_t k[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) k[i] = i * 256 + (int)threadIdx.x < count ? s.list[i * 256 + threadIdx.x] : 0;
+  for (int i = 0; i < PER; ++i) k[i] = i * T + (int)threadIdx.x < count ? s.list[i * T + threadIdx.x] : 0;
   __syncthreads();
   if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
@@ -126,20 +138,6 @@ __device__ __forceinline__ uint64_t prune(LogprobLds &s, int count, int n) {
   __syncthreads();
   return least;
 }
-// put(place, key) for the n largest keys of the list (fewer if it holds fewer), which
-// is complete behind a barrier.
-template <typename Put>
-__device__ __forceinline__ void ranked(LogprobLds &s, int n, Put &&put) {
-  if (s.count > kList) prune(s, s.count, n);
-  const int count = s.count;
-  for (int i = threadIdx.x; i < count; i += 256) {
-    const uint64_t k = s.list[i];
-    int rank = 0;
-    for (int j = 0; j < count; ++j) rank += s.list[j] > k;
-    if (rank < n) put(rank, k);
-  }
-}
-
 __device__ __forceinline__ void write_row(const LogprobArgs &a, int row, const Sums &s) {
   const long long token = a.token_bytes == 8 ? ((const long long *)a.tokens)[row] : ((const int32_t *)a.tokens)[row];
   float x = -INFINITY;
@@ -160,22 +158,18 @@ __device__ __forceinline__ void write_top(const LogprobArgs &a, int row, const S
   a.top_token[at] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
 }
 
-// Part blockIdx % parts of row first + blockIdx / parts.
-template <bool BF16>
-__global__ __launch_bounds__(256) void logprob_kernel(LogprobArgs a, int first) {
-  __shared__ LogprobLds s;
-  constexpr int E = BF16 ? 8 : 4, U = 4;         // elements of a vector, vectors at once
-  const int tid = threadIdx.x, part = (int)(blockIdx.x % (uint32_t)a.parts);
-  const int row = first + (int)(blockIdx.x / (uint32_t)a.parts);
+// A row a workgroup of T threads.
+template <bool BF16, int T>
+__global__ __launch_bounds__(T) void logprob_kernel(LogprobArgs a, int first) {
+  constexpr int E = BF16 ? 8 : 4, U = BF16 ? 4 : 8;        // elements of a vector, vectors at once
+  __shared__ LogprobLds<T, E> s;
+  const int tid = threadIdx.x, row = first + (int)blockIdx.x;
   const uint8_t *x = (const uint8_t *)a.logits + (long long)row * a.stride * (16 / E);
   // whole vectors from the first 16-byte border; the elements before and behind them
-  // (part 0) one by one
+  // one by one
   const int head = min((int)(-(uintptr_t)x & 15u) / (16 / E), a.vocab), vecs = (a.vocab - head) / E;
-  const int edges = part == 0 ? a.vocab - vecs * E : 0;
+  const int edges = a.vocab - vecs * E;
   const i32x4 *body = (const i32x4 *)(x + head * (16 / E));
-  // this part's rounds of 256 vectors
-  const int rounds = (vecs + 255) / 256;
-  const int r0 = (int)((long long)rounds * part / a.parts), r1 = (int)((long long)rounds * (part + 1) / a.parts);
 
   auto unpack = [&](const i32x4 &u, float *v) MOE_INLINE {
 #pragma unroll
@@ -188,57 +182,66 @@ __global__ __launch_bounds__(256) void logprob_kernel(LogprobArgs a, int first) 
       }
     }
   };
-  auto edge_at = [&]() MOE_INLINE { return tid < head ? tid : vecs * E + tid; };     // of tid < edges
-  auto edge = [&](int i) MOE_INLINE {
-    return BF16 ? bf16_to_f32(((const uint16_t *)x)[i]) : ((const float *)x)[i];
+  const int edge_at = tid < head ? tid : vecs * E + tid;   // of tid < edges
+  auto edge = [&]() MOE_INLINE {
+    return BF16 ? bf16_to_f32(((const uint16_t *)x)[edge_at]) : ((const float *)x)[edge_at];
   };
 
+  // rounds of T vectors, U at once
   Sums sum = {kNegBig, 0.0f, 0.0f};
-  int r = r0;
-  for (; (r + U - 1) * 256 + 255 < vecs && r + U <= r1; r += U) {
+  int r = 0;
+  for (; (r + U) * T <= vecs; r += U) {
     i32x4 u[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = body[(r + i) * 256 + tid];
+    for (int i = 0; i < U; ++i) u[i] = body[(r + i) * T + tid];
     float v[U * E];
 #pragma unroll
     for (int i = 0; i < U; ++i) unpack(u[i], v + i * E);
     add(sum, v);
   }
-  for (; r < r1; ++r)
-    if (r * 256 + tid < vecs) {
-      float v[E];
-      unpack(body[r * 256 + tid], v);
-      add(sum, v);
+  if (r * T < vecs) {                            // the last: what is past the end is no logit
+    i32x4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = body[min((r + i) * T + tid, vecs - 1)];
+    float v[U * E];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      unpack(u[i], v + i * E);
+      if ((r + i) * T + tid >= vecs) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[i * E + j] = -INFINITY;
+      }
     }
+    add(sum, v);
+  }
   // (the threads' maxima leave the edges out, which all go into the list)
   const uint32_t own = sum.m > kNegBig ? order_of(sum.m) : 0u;
   if (tid < edges) {
-    const float v[1] = {edge(edge_at())};
+    const float v[1] = {edge()};
     add(sum, v);
   }
-  const Sums all = join_group(sum, s.red);
-
-  uint64_t *keys = nullptr;
-  if (a.parts > 1) {
-    const long long unit = (long long)row * a.parts + part;
-    if (tid == 0) *(float4 *)(a.ws + unit * 16) = make_float4(all.m, all.l, all.t, 0.0f);
-    keys = (uint64_t *)(a.ws + (long long)a.rows * a.parts * 16) + unit * a.top;
-  } else if (tid == 0) {
-    write_row(a, row, all);
+  constexpr int GROUPS = LogprobLds<T, E>::groups;
+  if (a.top) {
+    uint32_t most = own;
+#pragma unroll
+    for (int m = 1; m < T / GROUPS; m <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, m, 64));
+    if (tid % (T / GROUPS) == 0) s.most[tid / (T / GROUPS)] = most;
+    if (tid == 0) s.owners = s.count = 0;
   }
+  const Sums all = join_group<T / 64>(sum, s.red);         // (with the barrier behind the maxima)
+  if (tid == T - 1) write_row(a, row, all);
   if (a.top == 0) return;
 
-  // The n-th largest of the threads' maxima, by the first wave, bit by bit.
-  s.most[tid] = own;
-  if (tid == 0) s.owners = s.count = 0;
-  __syncthreads();
+  // The n-th largest of the groups' maxima, by the first wave, bit by bit.
   if (tid < 64) {
-    const uint4 m = *(const uint4 *)&s.most[4 * tid];
-    uint32_t found = 0;
+    uint32_t m[GROUPS / 64], found = 0;
+#pragma unroll
+    for (int i = 0; i < GROUPS / 64; ++i) m[i] = s.most[64 * i + tid];
     for (int bit = 31; bit >= (BF16 ? 16 : 0); --bit) {
       const uint32_t trial = found | 1u << bit;
-      const int c = __popcll(__ballot(m.x >= trial)) + __popcll(__ballot(m.y >= trial)) +
-                    __popcll(__ballot(m.z >= trial)) + __popcll(__ballot(m.w >= trial));
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < GROUPS / 64; ++i) c += __popcll(__ballot(m[i] >= trial));
       if (c >= a.top) found = trial;
     }
     if (tid == 0) s.least = found;
@@ -250,72 +253,66 @@ __global__ __launch_bounds__(256) void logprob_kernel(LogprobArgs a, int first) 
     const uint64_t k = key_of(v, (uint32_t)i);
     if (k >= least) s.list[atomicAdd(&s.count, 1)] = k;
   };
-  if (tid < edges) push(edge(edge_at()), edge_at());
+  if (tid < edges) push(edge(), edge_at);
   __syncthreads();
-  const int owners = s.owners, items = owners * (r1 - r0);
-  for (int i0 = 0; i0 < items; i0 += 256) {
-    const int i = i0 + tid, vec = i < items ? (r0 + i / owners) * 256 + (int)s.owner[i % owners] : vecs;
+  const int owners = s.owners, items = vecs > 0 ? owners * ((vecs + T - 1) / T) : 0;
+  auto vec_of = [&](int i) MOE_INLINE { return i < items ? i / owners * T + (int)s.owner[i % owners] : vecs; };
+  int vec = vec_of(tid);
+  i32x4 u = body[min(vec, vecs - 1)];
+  for (int i0 = 0; i0 < items; i0 += T) {
+    // the next one is on its way while this one's go into the list
+    const int next = vec_of(i0 + T + tid);
+    const i32x4 un = body[min(next, vecs - 1)];
     if (vec < vecs) {
       float v[E];
-      unpack(body[vec], v);
+      unpack(u, v);
 #pragma unroll
       for (int j = 0; j < E; ++j) push(v[j], head + vec * E + j);
     }
+    vec = next;
+    u = un;
     __syncthreads();
     const int count = s.count;
     if (count > kList) least = prune(s, count, a.top);
     else __syncthreads();                        // all have read the count
   }
-  if (a.parts == 1) {
-    ranked(s, a.top, [&](int place, uint64_t key) { write_top(a, row, all, place, key); });
-  } else {
-    const int count = s.count;
-    if (tid < a.top && tid >= count) keys[tid] = 0;
-    ranked(s, a.top, [&](int place, uint64_t key) { keys[place] = key; });
+  // (the list holds at most kList keys, a.top at least: all of the row's that are not below `least`)
+  const int count = s.count;
+  for (int i = tid; i < count; i += T) {
+    const uint64_t k = s.list[i];
+    int rank = 0;
+    for (int j = 0; j < count; ++j) rank += s.list[j] > k;
+    if (rank < a.top) write_top(a, row, all, rank, k);
   }
 }
 
-// The parts of a row together.
-__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
-  __shared__ LogprobLds s;
-  const int tid = threadIdx.x, row = blockIdx.x;
-  Sums all = {kNegBig, 0.0f, 0.0f};
-  if (tid < a.parts) {
-    const float4 f = *(const float4 *)(a.ws + ((long long)row * a.parts + tid) * 16);
-    all = {f.x, f.y, f.z};
-  }
-  if (tid == 0) s.count = 0;
-  all = join_group(all, s.red);
-  if (tid == 0) write_row(a, row, all);
-  const uint64_t *keys = (const uint64_t *)(a.ws + (long long)a.rows * a.parts * 16) + (long long)row * a.parts * a.top;
-  for (int i = tid; i < a.parts * a.top; i += 256) {
-    const uint64_t k = keys[i];
-    if (k) s.list[atomicAdd(&s.count, 1)] = k;
-  }
-  __syncthreads();
-  if (a.top) ranked(s, a.top, [&](int place, uint64_t key) { write_top(a, row, all, place, key); });
+// Threads of a row.  Rows too few to keep the CUs busy: up to 1024 (64 rows of 120832
+// fp32: 15.2 us, 256 threads 21.2; 128 of 32003 bf16: 8.1 both; one of 8000 bf16: 64
+// threads 7.2, 256 5.4, 1024 7.4).  Many: what the steps behind the pass cost counts
+// (8192 rows of 1000 bf16: 64 threads 13.4 us, 256 31.7; of 8000: 34.6 and 35.5; 4096 of
+// 120832 with 20 alternatives: 342 and 237, 1024 threads 236, with one 206, 196 and 227).
+int threads_of_row(int rows, int vecs) {
+  if (rows < 512) return vecs >= 8192 ? 1024 : vecs >= 512 ? 256 : 64;
+  return vecs >= 1024 ? 256 : 64;
 }
 
-// Parts of a row: about 1024 workgroups, of 4 rounds of vectors each at least.
-int logprob_parts(int rows, int vocab, int is_bf16) {
-  const int rounds = vocab / (256 * (is_bf16 ? 8 : 4));
-  int p = 1024 / (rows > 0 ? rows : 1);
-  p = p < rounds / 4 ? p : rounds / 4;
-  return p < 1 ? 1 : p > kLogprobParts ? kLogprobParts : p;
-}
-
-hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s) {
-  const long long most = max_groups(256) / a.parts;
+template <bool BF16>
+hipError_t launch(const LogprobArgs &a, hipStream_t s) {
+  const int vecs = a.vocab / (BF16 ? 8 : 4), threads = threads_of_row(a.rows, vecs);
+  const long long most = max_groups(1024);
   for (long long row0 = 0; row0 < a.rows; row0 += most) {
-    const long long rows = a.rows - row0 < most ? a.rows - row0 : most;
-    const unsigned grid = (unsigned)(rows * a.parts);
-    if (a.is_bf16) logprob_kernel<true><<<grid, 256, 0, s>>>(a, (int)row0);
-    else logprob_kernel<false><<<grid, 256, 0, s>>>(a, (int)row0);
+    const unsigned rows = (unsigned)(a.rows - row0 < most ? a.rows - row0 : most);
+    if (threads == 1024) logprob_kernel<BF16, 1024><<<rows, 1024, 0, s>>>(a, (int)row0);
+    else if (threads == 256) logprob_kernel<BF16, 256><<<rows, 256, 0, s>>>(a, (int)row0);
+    else logprob_kernel<BF16, 64><<<rows, 64, 0, s>>>(a, (int)row0);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  if (a.parts > 1) logprob_join_kernel<<<(unsigned)a.rows, 256, 0, s>>>(a);     // (of 1024 rows at most)
-  return hipGetLastError();
+  return hipSuccess;
+}
+
+hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s) {
+  return a.is_bf16 ? launch<true>(a, s) : launch<false>(a, s);
 }
 
 }  // namespace moe

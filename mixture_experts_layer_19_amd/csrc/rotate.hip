@@ -9,8 +9,9 @@
 // `rotary` elements.  With the weight and the turn of a row folded into two factors an
 // element, y_j = (x_j c_j + x_partner s_j) / rms.
 //
-// The sum of squares is held in 64 bits (it does not overflow), 1 / rms as an fp32
-// number in (0.7, 1.5) and a power of two that x is multiplied by first; the angle in 64
+// The sum of squares is fp32, and taken again in 64 bits where it nears the ends of
+// fp32's range; 1 / rms is an fp32 number in (0.7, 1.5) and a power of two that x is
+// multiplied by first; the angle is held in 64
 // bits, reduced to a quarter turn before its sine and cosine are taken (their Taylor
 // series, whose first terms left out are below 2^-52) and rounded to fp32.  The rest is
 // fp32, and every output is rounded once from it.
@@ -141,11 +142,20 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int parts, in
         const int h = (sb + b) * HEADS + lane / L;
         float y[8];
         if constexpr (KIND < 2) {
-          double ss = 0.0;
+          float fs = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fma((double)v[b][j], (double)v[b][j], ss);
+          for (int j = 0; j < 8; ++j) fs = fmaf(v[b][j], v[b][j], fs);
 #pragma unroll
-          for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m, 64);
+          for (int m = 1; m < L; m <<= 1) fs += __shfl_xor(fs, m, 64);
+          double ss = fs;
+          // (2^-80: below it squares may have been lost that count)
+          if (__ballot(!(fs > 0x1p-80f && fs < INFINITY))) {
+            ss = 0.0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fma((double)v[b][j], (double)v[b][j], ss);
+#pragma unroll
+            for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m, 64);
+          }
           const double ms = ss * (1.0 / HD) + a.eps;
           // 1 / rms = r 2^-e, r of ms / 4^e, which is in [0.5, 2)
           const int e = __builtin_amdgcn_frexp_exp(ms) >> 1;

@@ -156,25 +156,17 @@ def test_linear_workspace_and_limits(B):
 # ----------------------------------------------------------------------------- log probabilities
 
 
-LOGPROBS = dict(x=P, dt=1, stride=1000, t=P, tb=4, rows=4, vocab=1000, top=5, lp=P, h=P, tl=P, tt=P, ws=P, size=1 << 30)
+LOGPROBS = dict(x=P, dt=1, stride=1000, t=P, tb=4, rows=4, vocab=1000, top=5, lp=P, h=P, tl=P, tt=P)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(x=P + 1), dict(dt=2), dict(t=None), dict(t=P + 2), dict(tb=2),
                                 dict(tb=8, t=P + 4), dict(rows=-1), dict(vocab=0), dict(top=-1), dict(top=65),
-                                dict(vocab=4), dict(lp=None), dict(h=P + 1), dict(tl=None), dict(tt=None),
-                                dict(ws=P + 8)])
+                                dict(vocab=4), dict(lp=None), dict(h=P + 1), dict(tl=None), dict(tt=None)])
 def test_logprobs_refuse(B, kw):
     refused(B, B.MOE_ERR_INVALID_ARG, B.moe_token_logprobs, *{**LOGPROBS, **kw}.values())
 
 
-def test_logprobs_workspace(B):
-    need = B.moe_token_logprobs_workspace_bytes(B.MOE_F32, 1, 120832, 20)
-    assert need > 0
-    few = {**LOGPROBS, "dt": B.MOE_F32, "rows": 1, "vocab": 120832, "top": 20}
-    refused(B, B.MOE_ERR_WORKSPACE, B.moe_token_logprobs, *{**few, "size": need - 1}.values())
-    refused(B, B.MOE_ERR_WORKSPACE, B.moe_token_logprobs, *{**few, "ws": None}.values())
-    assert B.moe_token_logprobs_workspace_bytes(B.MOE_BF16, 100000, 1000, 64) == 0
-    assert B.moe_token_logprobs_workspace_bytes(7, 4, 1000, 1) == 0
+def test_logprobs_of_no_rows(B):
     B.moe_token_logprobs(*{**LOGPROBS, "rows": 0, "x": None, "t": None}.values())
 
 
