@@ -9,9 +9,8 @@
 // `rotary` elements.  With the weight and the turn of a row folded into two factors an
 // element, y_j = (x_j c_j + x_partner s_j) / rms.
 //
-// The sum of squares is fp32, and taken again in 64 bits where it nears the ends of
-// fp32's range; 1 / rms is an fp32 number in (0.7, 1.5) and a power of two that x is
-// multiplied by first; the angle is held in 64
+// The mean of squares is fp32, and where it nears the ends of fp32's range taken again in
+// 64 bits, with x multiplied by a power of two near 1 / rms; the angle is held in 64
 // bits, reduced to a quarter turn before its sine and cosine are taken (their Taylor
 // series, whose first terms left out are below 2^-52) and rounded to fp32.  The rest is
 // fp32, and every output is rounded once from it.
@@ -147,27 +146,31 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int parts, in
           for (int j = 0; j < 8; ++j) fs = fmaf(v[b][j], v[b][j], fs);
 #pragma unroll
           for (int m = 1; m < L; m <<= 1) fs += __shfl_xor(fs, m, 64);
-          double ss = fs;
-          // (2^-80: below it squares may have been lost that count)
-          if (__ballot(!(fs > 0x1p-80f && fs < INFINITY))) {
-            ss = 0.0;
+          float ms = fmaf(fs, 1.0f / HD, a.eps);
+          int e = 0;
+          // squares that overflow, or are so small that some are lost: in 64 bits, with x
+          // multiplied by a power of two near 1 / rms first
+          if (__ballot(!(ms > 0x1p-80f && ms < 0x1p80f))) {
+            double ss = 0.0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fma((double)v[b][j], (double)v[b][j], ss);
 #pragma unroll
             for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m, 64);
+            ss = ss * (1.0 / HD) + a.eps;
+            e = __builtin_amdgcn_frexp_exp(ss) >> 1;
+            ms = (float)ldexp(ss, -2 * e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[b][j] = ldexpf(v[b][j], -e);
           }
-          const double ms = ss * (1.0 / HD) + a.eps;
-          // 1 / rms = r 2^-e, r of ms / 4^e, which is in [0.5, 2)
-          const int e = __builtin_amdgcn_frexp_exp(ms) >> 1;
-          const float m = (float)ldexp(ms, -2 * e);
-          const float r0 = __builtin_amdgcn_rsqf(m), t = fmaf(-m * r0, r0, 1.0f);
+          const float r0 = __builtin_amdgcn_rsqf(ms), t = fmaf(-ms * r0, r0, 1.0f);
           const float r = fabsf(t) < 1.0f ? fmaf(0.5f * r0, t, r0) : r0;     // (0, infinity and NaN as they are)
+          if (a.interleaved) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[b][j] = ldexpf(v[b][j], -e);
+            for (int j = 0; j < 8; ++j)
+              y[j] = fmaf(v[b][j], cw[j], d0 + j < a.rotary ? v[b][j ^ 1] * sw[j] : 0.0f) * r;
+          } else {                               // (what is not turned is its own partner, times 0)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float other = a.interleaved ? v[b][j ^ 1] : __shfl(v[b][j], partner, 64);
-            y[j] = fmaf(v[b][j], cw[j], (d0 + j < a.rotary ? other * sw[j] : 0.0f)) * r;
+            for (int j = 0; j < 8; ++j) y[j] = fmaf(v[b][j], cw[j], __shfl(v[b][j], partner, 64) * sw[j]) * r;
           }
         } else {
 #pragma unroll
@@ -226,7 +229,11 @@ hipError_t launch(const RotateArgs &a, hipStream_t s) {
   constexpr int HEADS = 64 / L;
   const int k_steps = (a.c.kv_heads + HEADS - 1) / HEADS;
   const int steps = (a.heads + HEADS - 1) / HEADS + (TO == TO_ROWS ? 1 : 2) * k_steps;
-  const int parts = (steps + 3) / 4;
+  // Steps of a wave: 4 as long as its waves are few (64 rows of 64 + 2 x 8 heads of 128
+  // into MX-fp8 6.0 us, with 10 steps 9.2), else 10, which find their row's place and
+  // turn half as often (8925 rows: 89.8 and 80.7 us; 8192 without a cache 72.7 and 60.6).
+  const int of_wave = (long long)a.c.rows * ((steps + 3) / 4) < 16384 ? 4 : 10;
+  const int parts = (steps + of_wave - 1) / of_wave;
   const long long most = max_groups(256) * 4 / parts;     // rows of a launch
   for (long long row0 = 0; row0 < a.c.rows; row0 += most) {
     const long long rows = a.c.rows - row0 < most ? a.c.rows - row0 : most;

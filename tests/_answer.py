@@ -99,8 +99,9 @@ def linear_ref(xq, xs, wq, ws, dtype):
 def turned(x, weight, positions, inv_freq, eps, interleaved, after):
     """(y, bound) of [rows, heads, head_dim] in f64.  The angle is the f64 product.
     Bound, before the output's rounding: relative to |a cos| + |b sin|, sines and cosines rounded to fp32
-    (1), the weight (1), the products and the sum (2), 1 / rms (3, and 1 where it is applied), the
-    mean of squares rounded (1), and 1 to spare, halves of a step each."""
+    (1), the product with the weight (1), the products and the sum (2), 1 / rms (3: the instruction's
+    step of 2, and its correction's rounding), its product (1), and the mean of squares, whose 8 additions in a
+    lane, 5 of lanes, division and eps, half of which reach the root (8); halves of a step each."""
     d, half = x.shape[2], inv_freq.numel()
     w = weight.double()
     n = x.double()
@@ -115,7 +116,7 @@ def turned(x, weight, positions, inv_freq, eps, interleaved, after):
     mag[..., lo], mag[..., hi] = (a * c).abs() + (b * s).abs(), (a * s).abs() + (b * c).abs()
     if after:
         y, mag = y * w, mag * w.abs()
-    return y, 10 * HALF * mag
+    return y, 16 * HALF * mag
 
 
 # ----------------------------------------------------------------------------- log probabilities
