@@ -52,15 +52,21 @@ __device__ __forceinline__ i32x8 fragment(const uint8_t *p) {
 __device__ __forceinline__ float block_scale(float am) {
   return am > 0.0f && am < INFINITY ? fmaxf(am * (1.0f / 448.0f), 0x1p-126f) : am == 0.0f ? 0.0f : __builtin_nanf("");
 }
-// E4M3 code of v / scale: the quotient in 64 bits (a multiplication by the inverse and a
-// correction, which makes quotients that 64 bits hold exact), then to the code by way of
-// fp32 rounded to odd, so that what lies next to the border of two codes falls on its side.
+// v / scale rounded to odd (towards zero, then the last bit set if anything was cut
+// off), from which the code, of 4 bits, is as if from the exact quotient: what lies next
+// to the border of two codes falls on its side.  A quotient within a step of the exact one,
+// and the sign of what is left, which a fused operation holds exactly: scales near the
+// lower end of fp32 are taken up from it with their values, and of values below
+// scale / 2^11, where it might be lost, the code is 0 anyway.  (In 64 bits, with three
+// conversions a value at a quarter of the rate: 8192 x 4096 27.3 us.)
 struct Quotient {
-  double scale, inv;
-  __device__ __forceinline__ Quotient(float s) : scale(s), inv(s == 0.0f ? 0.0 : 1.0 / (double)s) {}
+  float up, scale, inv;
+  __device__ __forceinline__ Quotient(float s) : up(s < 0x1p-70f ? 0x1p64f : 1.0f), scale(s * up),
+                                                 inv(s == 0.0f ? 0.0f : 1.0f / scale) {}
   __device__ __forceinline__ float operator()(float v) const {
-    const double q = (double)v * inv;
-    return round_f32<true>(fma(fma(-q, scale, (double)v), inv, q));
+    const float x = v * up, q0 = x * inv, q = fmaf(fmaf(-q0, scale, x), inv, q0), rest = fmaf(-q, scale, x);
+    const uint32_t b = __float_as_uint(q), below = (__float_as_uint(rest) ^ b) >> 31;   // the quotient is: one step down
+    return __uint_as_float(rest != 0.0f ? (b - below) | 1u : b);
   }
 };
 // 16 codes of 16 consecutive values
