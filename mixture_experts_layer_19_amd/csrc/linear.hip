@@ -334,12 +334,13 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
   const int s64 = wave % C::scales * 64;         // (more waves than that load the same ones)
   const uint32_t s_off = (min(tm * TM + s64 + lane, x16 * 16 - 1) - tm * TM) * 4;
   const float *col_scale = a.w_scale + (long long)min((tn * TN + wn * WN) / 128, (n16 - 1) / 8) * blocks;
-  auto load = [&](int b) MOE_INLINE {
+  // part i of a stage's loads: a block, behind the last one the scales
+  auto load_part = [&](int b, int i) MOE_INLINE {
     const uint32_t to = lds0 + (b & 1) * C::stage;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
+    if (i < PER)
       block_to_lds(to + min(wave * PER + i, C::blocks - 1) * kBlkBytes, src[i] + (long long)b * kBlkBytes, lane * 16);
-    word_to_lds(to + C::blocks * kBlkBytes + s64 * 4, row_scale + (long long)b * x16 * 16, s_off);
+    else
+      word_to_lds(to + C::blocks * kBlkBytes + s64 * 4, row_scale + (long long)b * x16 * 16, s_off);
   };
 
   // Fragments are read one row tile ahead, and a tile's products are added under the
@@ -369,12 +370,13 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
     for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(y[t & 1][j][i], f, acc[t][j][i]);
   };
 
-  load(0);
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) load_part(0, i);
   float sw = col_scale[0], sw_next = sw;
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   if (blocks > 1) {
     sw_next = col_scale[1];
-    load(1);
+    load_part(1, 0);
   }
   read_x(0, 0);
 #pragma unroll
@@ -385,6 +387,11 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
     for (int t = 0; t < MT; ++t) {
       const float own = sw;
       if (t + 1 < MT) {
+        if (MORE) {
+#pragma unroll
+          for (int i = 1; i <= PER; ++i)
+            if (i == t + 1 || (t + 2 == MT && i > t + 1)) load_part(b + 1, i);
+        }
         read_x(b, t + 1);
       } else if constexpr (MORE) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -392,7 +399,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
         sw = sw_next;
         if constexpr (decltype(left)::value > 1) {
           sw_next = col_scale[b + 2];
-          load(b + 2);
+          load_part(b + 2, 0);
         }
         read_x(b + 1, 0);
       }
