@@ -487,8 +487,9 @@ MOE_API moe_status moe_block_pack(const void *w, int dtype, int64_t row_stride, 
                           uint8_t *q, float *scale, void *stream);
 /* out [rows][n] contiguous, MOE_F32 or MOE_BF16.  x (MOE_F32 or MOE_BF16) is
  * quantised into ws first; with xq and xq_scale (of moe_block_quantize) x is
- * not used and no workspace is needed. */
-MOE_API size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k);
+ * not used.  ws: moe_block_linear_workspace_bytes() bytes (codes: whether xq is
+ * given; 0: none needed, or invalid arguments). */
+MOE_API size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k, int32_t codes);
 MOE_API moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, int32_t k,
                             const void *x, int x_dtype, int64_t x_stride, const uint8_t *xq,
                             const float *xq_scale, int32_t rows, void *out, int out_dtype,

@@ -129,7 +129,7 @@ def lib():
             "moe_block_packed_bytes": ([I32, I32], S),
             "moe_block_quantize": ([P, ctypes.c_int, I64, I32, I32, P, P, P], ctypes.c_int),
             "moe_block_pack": ([P, ctypes.c_int, I64, I32, I32, P, P, P], ctypes.c_int),
-            "moe_block_linear_workspace_bytes": ([I32, I32, I32], S),
+            "moe_block_linear_workspace_bytes": ([I32, I32, I32, I32], S),
             "moe_block_linear": ([P, P, I32, I32, P, ctypes.c_int, I64, P, P, I32, P, ctypes.c_int, P,
                                   S, P], ctypes.c_int),
             "moe_token_logprobs": ([P, ctypes.c_int, I64, P, I32, I32, I32, I32, P, P, P, P, P],
@@ -330,8 +330,8 @@ def moe_block_pack(w, dtype, row_stride, n, k, q, scale=None, stream=None):
     _check(lib().moe_block_pack(_ptr(w), dtype, row_stride, n, k, _ptr(q), _ptr(scale), _stream(stream)))
 
 
-def moe_block_linear_workspace_bytes(rows: int, n: int, k: int) -> int:
-    return lib().moe_block_linear_workspace_bytes(rows, n, k)
+def moe_block_linear_workspace_bytes(rows: int, n: int, k: int, codes: bool = False) -> int:
+    return lib().moe_block_linear_workspace_bytes(rows, n, k, int(codes))
 
 
 def moe_block_linear(wq, w_scale, n, k, x, x_dtype, x_stride, xq, xq_scale, rows, out, out_dtype, ws,

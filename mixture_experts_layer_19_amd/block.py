@@ -515,14 +515,14 @@ class BlockLinear(_Bound):
         n = self.out_features
         out = torch.empty_strided((rows, n), (n, 1), dtype=self.out_dtype, device=dev)
         xp = xs = qp = sp = wp = 0
-        size, ws = 0, None
         if codes is not None:
             qp, sp = codes.q.data_ptr(), codes.scale.data_ptr()
         else:
-            xp, xs, size = x.data_ptr(), x.stride(0), self._bytes(rows, n, k)
-            if size:
-                ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=dev)
-                wp = ws.data_ptr()
+            xp, xs = x.data_ptr(), x.stride(0)
+        size, ws = self._bytes(rows, n, k, codes is not None), None
+        if size:
+            ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=dev)
+            wp = ws.data_ptr()
         rc = self._call(self._w, self._ws, n, k, xp, self._in, xs, qp, sp, rows, out.data_ptr(), self._out, wp, size,
                         _raw_stream(dev.index))
         if rc:

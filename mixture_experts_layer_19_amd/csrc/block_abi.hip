@@ -288,9 +288,13 @@ moe_status moe_block_pack(const void *w, int dtype, int64_t row_stride, int32_t 
   return done(launch_block_pack(w, row_stride, src, n, k, q, scale, (hipStream_t)stream));
 }
 
-size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k) {
+size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k, int32_t codes) {
   if (!blocked(rows) || !blocked(n) || !blocked(k)) return 0;
-  return moe_block_packed_bytes(rows, k) + scale_bytes(rows, k);
+  LinearArgs a = {};
+  a.rows = rows;
+  a.n = n;
+  a.k = k;
+  return linear_part_bytes(a) + (codes ? 0 : moe_block_packed_bytes(rows, k) + scale_bytes(rows, k));
 }
 
 moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, int32_t k, const void *x,
@@ -303,19 +307,22 @@ moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, 
   if (!wq || !al(wq, 16) || !w_scale || !al(w_scale, 4) || !out || !al(out, 16) || !al(xq, 16) || !al(xq_scale, 16) ||
       !al(ws, 16))
     return MOE_ERR_INVALID_ARG;
-  if (!linear_fits(rows, n)) return MOE_ERR_UNSUPPORTED;
+  if (!xq && (!x || !al(x, x_dtype == MOE_F32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
+  LinearArgs a = {xq, xq_scale, wq, w_scale, out, rows, n, k, nullptr, 1};
+  if (!linear_fits(a)) return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_block_linear_workspace_bytes(rows, n, k, xq != nullptr);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  a.splits = linear_splits(a);
+  a.part = (float *)ws;
   if (!xq) {
-    if (!x || !al(x, x_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
-    if (!ws || ws_bytes < moe_block_linear_workspace_bytes(rows, n, k)) return MOE_ERR_WORKSPACE;
-    uint8_t *q = (uint8_t *)ws;
+    uint8_t *q = (uint8_t *)ws + linear_part_bytes(a);
     float *scale = (float *)(q + moe_block_packed_bytes(rows, k));
     const hipError_t err =
         launch_block_quantize(x, x_stride, x_dtype == MOE_BF16, rows, k, q, scale, (hipStream_t)stream);
     if (err != hipSuccess) return MOE_ERR_DEVICE;
-    xq = q;
-    xq_scale = scale;
+    a.q = q;
+    a.q_scale = scale;
   }
-  const LinearArgs a = {xq, xq_scale, wq, w_scale, out, rows, n, k};
   return done(launch_linear(a, out_dtype == MOE_F32, (hipStream_t)stream));
 }
 

@@ -89,13 +89,18 @@ struct LinearArgs {
   const float *w_scale;        // [n / 128][k / 128]
   void *out;                   // [rows][n]
   int rows, n, k;
+  float *part;                 // splits > 1: fp32 sums [splits][rows][n up to a multiple of 4]
+  int splits;                  // linear_splits of the sizes
 };
 hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, int rows, int cols, uint8_t *q,
                                  float *scale, hipStream_t stream);
 // src: FMT_F32, FMT_BF16 (scales are written) or FMT_FP8 (codes, which only change places).
 hipError_t launch_block_pack(const void *w, long long stride, int src, int n, int cols, uint8_t *q, float *scale,
                              hipStream_t stream);
-bool linear_fits(int rows, int n);        // within one launch's workgroups
+// These read the sizes alone.
+int linear_splits(const LinearArgs &a);
+size_t linear_part_bytes(const LinearArgs &a);   // workspace of the splits (0: none)
+bool linear_fits(const LinearArgs &a);           // within one launch's workgroups
 hipError_t launch_linear(const LinearArgs &a, int f32_out, hipStream_t stream);
 
 // Token log probabilities (logprobs.hip).

@@ -305,7 +305,8 @@ __device__ __forceinline__ void word_to_lds(uint32_t to, const void *base, uint3
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
 }
 
-template <bool F32, int TM, int TN, int WM, int WN>
+// SPLIT: a.splits workgroups share a tile's blocks and leave fp32 sums in a.part.
+template <bool F32, int TM, int TN, int WM, int WN, bool SPLIT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kernel(LinearArgs a, int tiles_m, int tiles_n) {
   using C = TileCfg<TM, TN, WM, WN>;
   constexpr int MT = WM / 16, NT = WN / 16, PER = (C::blocks + C::waves - 1) / C::waves, GROUP = 4;
@@ -317,8 +318,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
 
   // Workgroups go round the eight XCDs; each takes a run of tiles, GROUP row tiles by
   // all column tiles at a time, so that those that run together share its L2.
-  const int total = tiles_m * tiles_n, per = (total + 7) / 8, tile = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (tile >= total) return;
+  const int total = tiles_m * tiles_n, units = SPLIT ? total * a.splits : total, per = (units + 7) / 8;
+  const int unit = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (unit >= units) return;
+  const int split = SPLIT ? unit / total : 0, tile = unit - split * total;
+  const int begin = SPLIT ? (int)((long long)blocks * split / a.splits) : 0;
+  const int end = SPLIT ? (int)((long long)blocks * (split + 1) / a.splits) : blocks;
   const int first = tile / (GROUP * tiles_n) * GROUP, group = min(GROUP, tiles_m - first), in = tile - first * tiles_n;
   const int tm = first + in % group, tn = in / group;
 
@@ -371,16 +376,16 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
   };
 
 #pragma unroll
-  for (int i = 0; i <= PER; ++i) load_part(0, i);
-  float sw = col_scale[0], sw_next = sw;
+  for (int i = 0; i <= PER; ++i) load_part(begin, i);
+  float sw = col_scale[begin], sw_next = sw;
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (blocks > 1) {
-    sw_next = col_scale[1];
-    load_part(1, 0);
+  if (end - begin > 1) {
+    sw_next = col_scale[begin + 1];
+    load_part(begin + 1, 0);
   }
-  read_x(0, 0);
+  read_x(begin, 0);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) read_w(0, j);
+  for (int j = 0; j < NT; ++j) read_w(begin, j);
   auto block = [&](int b, auto left) MOE_INLINE {
     constexpr bool MORE = decltype(left)::value > 0;       // another block behind it, and one more
 #pragma unroll
@@ -427,13 +432,13 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
         asm volatile("" : "+v"(sum));
       }
   };
-  for (int b = 0; b + 2 < blocks; ++b) block(b, std::integral_constant<int, 2>{});
-  if (blocks > 1) block(blocks - 2, std::integral_constant<int, 1>{});
-  block(blocks - 1, std::integral_constant<int, 0>{});
+  for (int b = begin; b + 2 < end; ++b) block(b, std::integral_constant<int, 2>{});
+  if (end - begin > 1) block(end - 2, std::integral_constant<int, 1>{});
+  block(end - 1, std::integral_constant<int, 0>{});
 #pragma unroll
   for (int j = 0; j < NT; ++j) add_up(MT - 1, j);
   // the tile's rows out
-  if (!F32 && a.n % 8 == 0) {
+  if (!F32 && !SPLIT && a.n % 8 == 0) {
     // By way of the LDS, a wave's rows by themselves, so that a store is 16 bytes a lane
     // and whole lines: 16-byte pieces of a row lie turned by the row, which spreads the
     // banks.
@@ -459,27 +464,44 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
     }
     return;
   }
+  if constexpr (SPLIT) {
+    a.n = (a.n + 3) / 4 * 4;
+    a.out = a.part + (long long)split * a.rows * a.n;
+  }
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const long long r = (long long)tm * TM + wm * WM + t * 16 + (lane & 15);
     if (r < a.rows)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) store4<F32>(a, r, tn * TN + wn * WN + j * 16 + 4 * (lane >> 4), acc[t][j]);
+      for (int j = 0; j < NT; ++j) store4<F32 || SPLIT>(a, r, tn * TN + wn * WN + j * 16 + 4 * (lane >> 4), acc[t][j]);
   }
+}
+
+// The splits' sums together, in their order: four columns a thread.
+template <bool F32>
+__global__ __launch_bounds__(256) void block_join_kernel(LinearArgs a) {
+  const int n4 = (a.n + 3) / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, size = (long long)a.rows * n4;
+  if (i >= size) return;
+  f32x4 y = *(const f32x4 *)(a.part + 4 * i);
+  for (int s = 1; s < a.splits; ++s) y += *(const f32x4 *)(a.part + 4 * (s * size + i));
+  store4<F32>(a, i / n4, (int)(i % n4) * 4, y);
 }
 
 // ----------------------------------------------------------------------------- launches
 
 namespace {
-template <bool F32, int TM, int TN, int WM, int WN>
+template <bool F32, int TM, int TN, int WM, int WN, bool SPLIT = false>
 hipError_t tiles(const LinearArgs &a, hipStream_t s) {
   using C = TileCfg<TM, TN, WM, WN>;
   static OncePerDevice once;
-  const auto kernel = block_tile_kernel<F32, TM, TN, WM, WN>;
+  const auto kernel = block_tile_kernel<F32, TM, TN, WM, WN, SPLIT>;
   const hipError_t err = allow_lds(once, (const void *)kernel, C::lds);
   if (err != hipSuccess) return err;
   const int tm = (a.rows + TM - 1) / TM, tn = (a.n + TN - 1) / TN;
-  kernel<<<(unsigned)(((long long)tm * tn + 7) / 8 * 8), C::threads, C::lds, s>>>(a, tm, tn);
+  kernel<<<(unsigned)(((long long)tm * tn * (SPLIT ? a.splits : 1) + 7) / 8 * 8), C::threads, C::lds, s>>>(a, tm, tn);
+  if (SPLIT)
+    block_join_kernel<F32><<<(unsigned)(((long long)a.rows * ((a.n + 3) / 4) + 255) / 256), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -511,23 +533,47 @@ hipError_t few(const LinearArgs &a, hipStream_t s) {
          : RT == 1 ? few<F32, RT, 1, 4>(a, s) : few<F32, RT, 1, 8>(a, s);
 }
 
+// Which tiles: 256 or 128 square by how full their rounds are, one of the former or two of
+// the latter a CU, which run at 0.8 of the speed (8192 rows, 10240 columns, k = 4096: 307
+// and 378 us; 1024, 10240, 4096: 51 and 64; 2048, 4096, 8192: 92 and 76); 64 square up
+// to 128 of 128 square (128, 10240, 4096: 20.7 us, 128 square 25.3; 300, 16384, 1024: 15.1 and
+// 11.9).
+long long count(const LinearArgs &a, int t) { return ((a.rows + t - 1ll) / t) * ((a.n + t - 1ll) / t); }
+int tile_of(const LinearArgs &a) {
+  if (a.rows <= 64) return 64;
+  const long long t128 = count(a, 128), t256 = count(a, 256);
+  if (t128 <= 128) return 64;
+  auto full = [](long long t, long long slots) { return (double)t / (double)((t + slots - 1) / slots * slots); };
+  return full(t256, 256) >= 0.8 * full(t128, 512) ? 256 : 128;
+}
+
 template <bool F32>
 hipError_t linear(const LinearArgs &a, hipStream_t s) {
-  if (a.rows > 64) {
-    const long long big = ((a.rows + 255ll) / 256) * ((a.n + 255ll) / 256);
-#ifdef TST
-    return tiles<F32, TST>(a, s);
-#endif
-    return big >= 256 ? tiles<F32, 256, 256, 128, 64>(a, s) : tiles<F32, 128, 128, 64, 64>(a, s);
-  }
-  if (a.rows > 32 && a.n >= 32768) return tiles<F32, 64, 64, 64, 32>(a, s);
-  return a.rows <= 16 ? few<F32, 1>(a, s) : a.rows <= 32 ? few<F32, 2>(a, s) : few<F32, 4>(a, s);
+  if (a.rows <= 64 && (a.rows <= 32 || a.n < 32768))
+    return a.rows <= 16 ? few<F32, 1>(a, s) : a.rows <= 32 ? few<F32, 2>(a, s) : few<F32, 4>(a, s);
+  const int tile = tile_of(a);
+  if (a.splits > 1) return tiles<F32, 64, 64, 64, 32, true>(a, s);
+  return tile == 256 ? tiles<F32, 256, 256, 128, 64>(a, s)
+         : tile == 128 ? tiles<F32, 128, 128, 64, 64>(a, s) : tiles<F32, 64, 64, 64, 32>(a, s);
 }
 }  // namespace
 
-bool linear_fits(int rows, int n) {
-  const long long n16 = (n + 15ll) / 16, tiles = ((rows + 127ll) / 128) * ((n + 127ll) / 128);
-  return rows <= 64 ? n16 <= max_groups(256) : tiles + 8 <= max_groups(512);
+// Workgroups that share a tile's blocks: some 512 in all, with 8 blocks each at least
+// (200 rows, 180 columns, k = 4096: 8.3 us, whole 14.0; 256, 4096, 8192: 26.8 and 36.7;
+// with half the blocks each 1000, 260, 1024 takes 7.4 us, whole 5.6).
+int linear_splits(const LinearArgs &a) {
+  if (a.rows <= 64 || tile_of(a) != 64) return 1;
+  const long long t = count(a, 64), blocks = (a.k + (kBlk - 1ll)) / kBlk;
+  const long long s = 512 / t < blocks / 8 ? 512 / t : blocks / 8;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+size_t linear_part_bytes(const LinearArgs &a) {
+  const int s = linear_splits(a);
+  return s == 1 ? 0 : (size_t)s * a.rows * ((a.n + 3ll) / 4 * 4) * 4;
+}
+bool linear_fits(const LinearArgs &a) {
+  // (workgroups of at most 512 threads; 64 square tiles beyond 64 rows are few)
+  return (a.rows <= 64 ? (a.n + 15ll) / 16 : count(a, 128)) + 8 <= max_groups(512);
 }
 
 hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, int rows, int cols, uint8_t *q,

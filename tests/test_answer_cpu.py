@@ -105,6 +105,8 @@ def test_sizes(B):
     assert B.moe_block_packed_bytes(1 << 20, 1 << 20) == 1 << 40
     assert B.moe_block_linear_workspace_bytes(0, 5, 5) == 0
     assert B.moe_block_linear_workspace_bytes(17, 5, 129) >= 2 * 2 * 2048 + 2 * 32 * 4
+    assert B.moe_block_linear_workspace_bytes(17, 5, 129, codes=True) == 0
+    assert B.moe_block_linear_workspace_bytes(70, 100, 8192, codes=True) > 0       # split blocks
 
 
 @pytest.mark.parametrize("kw", [dict(dt=2), dict(rows=-1), dict(cols=0), dict(x=None), dict(x=P + 1), dict(q=None),
@@ -148,6 +150,9 @@ def test_linear_workspace_and_limits(B):
     need = B.moe_block_linear_workspace_bytes(8, 256, 512)
     refused(B, B.MOE_ERR_WORKSPACE, B.moe_block_linear, *{**LINEAR, "size": need - 1}.values())
     refused(B, B.MOE_ERR_WORKSPACE, B.moe_block_linear, *{**LINEAR, "ws": None}.values())
+    split = {**LINEAR, "rows": 70, "n": 100, "k": 8192, "x": None, "xs": 0, "xq": P, "xqs": P}
+    need = B.moe_block_linear_workspace_bytes(70, 100, 8192, codes=True)
+    refused(B, B.MOE_ERR_WORKSPACE, B.moe_block_linear, *{**split, "size": need - 1}.values())
     refused(B, B.MOE_ERR_UNSUPPORTED, B.moe_block_linear, *{**LINEAR, "k": (1 << 30) + 1}.values())
     refused(B, B.MOE_ERR_UNSUPPORTED, B.moe_block_linear, *{**LINEAR, "rows": 1 << 30, "n": 1 << 30}.values())
     B.moe_block_linear(*{**LINEAR, "rows": 0, "x": None, "out": None, "ws": None}.values())

@@ -117,6 +117,26 @@ def test_product(act, out, rows, n, k):
     assert torch.equal(again(x.cuda()), y)
 
 
+# every way a product is cut up: columns of a workgroup, the square tiles, split blocks
+WAYS = [
+    (5, 10230, 260), (20, 10230, 260), (50, 10240, 260), (3, 16380, 300), (31, 16384, 128), (64, 16377, 300),
+    (40, 33000, 200), (64, 32777, 130), (33, 32768, 384), (1500, 1500, 300), (1409, 1531, 128), (2100, 3904, 300),
+    (2090, 3901, 256), (70, 100, 4100), (65, 16, 16384), (200, 180, 2048), (130, 4097, 2100), (600, 70, 2500),
+]
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,n,k", WAYS)
+def test_ways_of_the_product(out, rows, n, k):
+    g = gen(rows + n + k)
+    x = rows_of(g, rows, k, BF16)
+    codes, scale = weight_of(g, n, k)
+    lin = block.BlockLinear(codes.cuda(), scale.cuda(), out_dtype=out)
+    y = lin(x.cuda())
+    check(lin, x, codes.double(), scale, y)
+    assert torch.equal(lin(codes=lin.quantize(x.cuda())), y)
+
+
 @pytest.mark.parametrize("act", [BF16, F32])
 def test_rows_are_independent(act):
     """A row's result does not go by the rows beside it beyond the additions' order, and
@@ -172,12 +192,12 @@ def test_no_rows_and_large_and_small_values():
     assert (y[4] == 0).all()
 
 
-@pytest.mark.parametrize("rows", [1, 64, 300])
-def test_captured_and_on_another_stream(rows):
+@pytest.mark.parametrize("rows,k", [(1, 640), (64, 640), (300, 640), (300, 4096), (2500, 256)])
+def test_captured_and_on_another_stream(rows, k):
     g = gen(rows)
-    codes, scale = weight_of(g, 272, 640)
+    codes, scale = weight_of(g, 1272, k)
     lin = block.BlockLinear(codes.cuda(), scale.cuda())
-    xs = [rows_of(g, rows, 640, BF16).cuda() for _ in range(3)]
+    xs = [rows_of(g, rows, k, BF16).cuda() for _ in range(3)]
     want = [lin(x).clone() for x in xs]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
