@@ -476,8 +476,8 @@ MOE_API moe_status moe_head_norm_rope_write(const moe_head_norm *norm /* host */
  * [cols / 128][rows rounded up to 16], weight scales [n / 128][k / 128].
  * rows, n, k up to 2^30. */
 MOE_API size_t moe_block_packed_bytes(int32_t rows, int32_t cols);
-/* Activations x (MOE_F32 or MOE_BF16, any alignment of an element and row stride;
- * 16 bytes are faster) to packed codes and scales. */
+/* Activations x (MOE_F32 or MOE_BF16, an element's alignment, any row stride) to
+ * packed codes and scales. */
 MOE_API moe_status moe_block_quantize(const void *x, int dtype, int64_t row_stride, int32_t rows, int32_t cols,
                               uint8_t *q, float *scale, void *stream);
 /* Weights to packed codes: MOE_F32 or MOE_BF16 are quantised, their scales written;

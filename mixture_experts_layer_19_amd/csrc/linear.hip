@@ -77,15 +77,25 @@ __device__ __forceinline__ i32x4 codes16(const float (&v)[16], const Quotient &q
     r[j] = (int)e4m3_pack4(q(v[4 * j]), q(v[4 * j + 1]), q(v[4 * j + 2]), q(v[4 * j + 3]));
   return r;
 }
-// n of 16 consecutive elements of a row, the rest 0
-template <bool BF16, bool VEC>
+// n of 16 consecutive elements of a row, the rest 0.  (Vector loads need only an element's
+// alignment; a row that starts between two 16-byte borders takes some lines twice.)
+typedef i32x4 __attribute__((aligned(2))) i32x4_at2;
+typedef i32x4 __attribute__((aligned(4))) i32x4_at4;
+template <bool BF16>
 __device__ __forceinline__ void load16(const void *p, long long i, int n, float (&v)[16]) {
-  if (VEC && n >= 16) {
-    float a[8], b[8];
-    load8<BF16>(p, i, a);
-    load8<BF16>(p, i + 8, b);
+  if (n >= 16) {
+    if constexpr (BF16) {
+      const i32x4_at2 *at = (const i32x4_at2 *)((const uint16_t *)p + i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = a[j], v[8 + j] = b[j];
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t w = (uint32_t)at[j / 8][j / 2 % 4];
+        v[j] = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+      }
+    } else {
+      const i32x4_at4 *at = (const i32x4_at4 *)((const float *)p + i);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __int_as_float(at[j / 4][j % 4]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -109,7 +119,7 @@ __device__ __forceinline__ float largest16(const float (&v)[16]) {
 }
 
 // Activations: a wave takes 8 rows of one block, 8 lanes a row, 16 elements a lane.
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void block_quantize_kernel(const void *x, long long stride, int rows, int cols,
                                                              uint8_t *q, float *scale, int first) {
   const int blocks = (cols + kBlk - 1) / kBlk, rows16 = (rows + 15) / 16 * 16;
@@ -119,7 +129,7 @@ __global__ __launch_bounds__(256) void block_quantize_kernel(const void *x, long
   if (row >= rows16) return;
   const int k = b * kBlk + 16 * i;
   float v[16];
-  load16<BF16, VEC>(x, row * stride + k, row < rows ? min(cols - k, 16) : 0, v);
+  load16<BF16>(x, row * stride + k, row < rows ? min(cols - k, 16) : 0, v);
   float am = largest16(v);
 #pragma unroll
   for (int m = 1; m < 8; m <<= 1) am = fmaxf(am, __shfl_xor(am, m, 64));
@@ -143,7 +153,7 @@ __global__ __launch_bounds__(128) void block_pack_kernel(const void *w, long lon
   float am = 0.0f, v[16];
   if constexpr (!CODES) {
     for (long long row = row0 + (tid >> 3); row < row0 + kBlk && row < n; row += 16) {
-      load16<BF16, false>(w, row * stride + k, min(cols - k, 16), v);
+      load16<BF16>(w, row * stride + k, min(cols - k, 16), v);
       am = fmaxf(am, largest16(v));
     }
 #pragma unroll
@@ -165,7 +175,7 @@ __global__ __launch_bounds__(128) void block_pack_kernel(const void *w, long lon
         for (int j = 0; j < 16; ++j) to[j] = j < have ? from[j] : 0;
       }
     } else {
-      load16<BF16, false>(w, row * stride + k, have, v);
+      load16<BF16>(w, row * stride + k, have, v);
       *(i32x4 *)to = codes16(v, quot);
     }
   }
@@ -174,17 +184,19 @@ __global__ __launch_bounds__(128) void block_pack_kernel(const void *w, long lon
 
 // ----------------------------------------------------------------------------- products
 
-// Four neighbouring columns n .. n + 3 of row r (those below a.n).
+// Four neighbouring columns n .. n + 3 of row r (those below a.n), at any alignment of an
+// element.
+typedef uint2 __attribute__((aligned(2))) uint2_at2;
+typedef f32x4 __attribute__((aligned(4))) f32x4_at4;
 template <bool F32>
 __device__ __forceinline__ void store4(const LinearArgs &a, long long r, int n, const f32x4 &y) {
   const long long at = r * a.n + n;
-  if (a.n % 4 == 0) {
-    if (n >= a.n) return;
-    if constexpr (F32) *(f32x4 *)((float *)a.out + at) = y;
-    else *(uint2 *)((uint16_t *)a.out + at) = make_uint2(bf16_pack2(y[0], y[1]), bf16_pack2(y[2], y[3]));
+  if (n + 4 <= a.n) {
+    if constexpr (F32) *(f32x4_at4 *)((float *)a.out + at) = y;
+    else *(uint2_at2 *)((uint16_t *)a.out + at) = make_uint2(bf16_pack2(y[0], y[1]), bf16_pack2(y[2], y[3]));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
       if (n + i < a.n) {
         if constexpr (F32) ((float *)a.out)[at + i] = y[i];
         else ((uint16_t *)a.out)[at + i] = (uint16_t)bf16_pack2(y[i], 0.0f);
@@ -348,6 +360,15 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
       word_to_lds(to + C::blocks * kBlkBytes + s64 * 4, row_scale + (long long)b * x16 * 16, s_off);
   };
 
+  // A stage's loads: all at once as soon as its place is free, or, where the products
+  // take longer than the loads, spread over the block before it, a part every row tile
+  // (256 square: 325 -> 307 us; 64 square, 64 rows by 120832: 114 -> 124).
+  constexpr bool SPREAD = MT >= 8;
+  auto load_ahead = [&](int b) MOE_INLINE {
+#pragma unroll
+    for (int i = 0; i <= (SPREAD ? 0 : PER); ++i) load_part(b, i);
+  };
+
   // Fragments are read one row tile ahead, and a tile's products are added under the
   // next one's: in this order, which the compiler's own is slower than.  Before the last
   // row tile of a block everything of it is in registers: there all waves meet, the
@@ -381,7 +402,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   if (end - begin > 1) {
     sw_next = col_scale[begin + 1];
-    load_part(begin + 1, 0);
+    load_ahead(begin + 1);
   }
   read_x(begin, 0);
 #pragma unroll
@@ -392,7 +413,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
     for (int t = 0; t < MT; ++t) {
       const float own = sw;
       if (t + 1 < MT) {
-        if (MORE) {
+        if (MORE && SPREAD) {
 #pragma unroll
           for (int i = 1; i <= PER; ++i)
             if (i == t + 1 || (t + 2 == MT && i > t + 1)) load_part(b + 1, i);
@@ -404,7 +425,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
         sw = sw_next;
         if constexpr (decltype(left)::value > 1) {
           sw_next = col_scale[b + 2];
-          load_part(b + 2, 0);
+          load_ahead(b + 2);
         }
         read_x(b + 1, 0);
       }
@@ -438,7 +459,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
 #pragma unroll
   for (int j = 0; j < NT; ++j) add_up(MT - 1, j);
   // the tile's rows out
-  if (!F32 && !SPLIT && a.n % 8 == 0) {
+  if constexpr (!F32 && !SPLIT) {
     // By way of the LDS, a wave's rows by themselves, so that a store is 16 bytes a lane
     // and whole lines: 16-byte pieces of a row lie turned by the row, which spreads the
     // banks.
@@ -460,7 +481,14 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
       const int r = i * (64 / PIECES) + lane / PIECES;
       const long long row = (long long)tm * TM + wm * WM + r;
       const i32x4 v = *(const i32x4 *)(own + (r * PIECES + (piece ^ (r % PIECES))) * 16);
-      if (row < a.rows && n < a.n) *(i32x4 *)((uint16_t *)a.out + row * a.n + n) = v;
+      uint16_t *to = (uint16_t *)a.out + row * a.n + n;
+      if (row < a.rows && n + 8 <= a.n) {
+        *(i32x4_at2 *)to = v;
+      } else if (row < a.rows) {
+#pragma unroll
+        for (int c = 0; c < 7; ++c)
+          if (n + c < a.n) to[c] = (uint16_t)((uint32_t)v[c / 2] >> (16 * (c & 1)));
+      }
     }
     return;
   }
@@ -579,18 +607,15 @@ bool linear_fits(const LinearArgs &a) {
 hipError_t launch_block_quantize(const void *x, long long stride, int is_bf16, int rows, int cols, uint8_t *q,
                                  float *scale, hipStream_t s) {
   const int blocks = (int)((cols + (kBlk - 1ll)) / kBlk);
-  const long long rows16 = (rows + 15ll) / 16 * 16, e = is_bf16 ? 8 : 4;
-  const bool vec = ((uintptr_t)x & 15) == 0 && (rows == 1 || stride % e == 0);
+  const long long rows16 = (rows + 15ll) / 16 * 16;
   // rows of a launch: a multiple of 8
   long long most = max_groups(256) * 4 / blocks * 8;
   if (most == 0) return hipErrorInvalidValue;
   for (long long row0 = 0; row0 < rows16; row0 += most) {
     const long long n = rows16 - row0 < most ? rows16 - row0 : most;
     const unsigned grid = (unsigned)((n / 8 * blocks + 3) / 4);
-    if (is_bf16 && vec) block_quantize_kernel<true, true><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
-    else if (is_bf16) block_quantize_kernel<true, false><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
-    else if (vec) block_quantize_kernel<false, true><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
-    else block_quantize_kernel<false, false><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
+    if (is_bf16) block_quantize_kernel<true><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
+    else block_quantize_kernel<false><<<grid, 256, 0, s>>>(x, stride, rows, cols, q, scale, (int)row0);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
