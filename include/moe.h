@@ -446,7 +446,7 @@ MOE_API moe_status moe_head_norm_rope(const moe_head_norm *norm /* host */, cons
                               int32_t rows, void *q_out, void *k_out, void *stream);
 /* The same for the rows of a batch at their positions, with the turned keys and the
  * values v written into the cache, as moe_kv_write would (an MX-fp8 cache takes
- * the codes of the keys before their rounding to bf16).  q_out: zeros for rows of no sequence,
+ * the codes of the keys from 64 bits, not from their rounding to bf16).  q_out: zeros for rows of no sequence,
  * before its start or past its table; keys and values of rows without a page are
  * dropped.  The norm's dtype is that of the cache's activations, its head_dim the
  * cache's. */
