@@ -374,7 +374,7 @@ class HeadNormRope(_Bound):
     def __call__(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, stream=None):
         """(q, k) [rows, heads, head_dim] and [rows, kv_heads, head_dim] (row and head
         strides in whole 16-byte pieces), normed and turned to positions [rows] int32."""
-        rows = q.shape[0]
+        rows = q.shape[0] if q.dim() else 0
         self._check(q, rows, "q")
         self._check(k, rows, "k")
         if positions.shape != (rows,) or positions.dtype != torch.int32 or not positions.is_contiguous() \

@@ -144,10 +144,10 @@ __global__ __launch_bounds__(256) void block_quantize_kernel(const void *x, long
 // CODES: they are codes already and only change places.
 template <bool BF16, bool CODES>
 __global__ __launch_bounds__(128) void block_pack_kernel(const void *w, long long stride, int n, int cols, uint8_t *q,
-                                                         float *scale, int first) {
+                                                         float *scale) {
   __shared__ float red[2];
   const int blocks = (cols + kBlk - 1) / kBlk, tid = threadIdx.x;
-  const long long unit = (long long)first + blockIdx.x;
+  const long long unit = blockIdx.x;
   const int b = (int)(unit % blocks), i = tid & 7, k = b * kBlk + 16 * i, n16 = (n + 15) / 16 * 16;
   const long long row0 = unit / blocks * kBlk;
   float am = 0.0f, v[16];
@@ -626,9 +626,9 @@ hipError_t launch_block_pack(const void *w, long long stride, int src, int n, in
                              hipStream_t s) {
   const long long units = ((n + (kBlk - 1ll)) / kBlk) * ((cols + (kBlk - 1ll)) / kBlk);
   const unsigned grid = (unsigned)units;
-  if (src == FMT_FP8) block_pack_kernel<false, true><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale, 0);
-  else if (src == FMT_BF16) block_pack_kernel<true, false><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale, 0);
-  else block_pack_kernel<false, false><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale, 0);
+  if (src == FMT_FP8) block_pack_kernel<false, true><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale);
+  else if (src == FMT_BF16) block_pack_kernel<true, false><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale);
+  else block_pack_kernel<false, false><<<grid, 128, 0, s>>>(w, stride, n, cols, q, scale);
   return hipGetLastError();
 }
 

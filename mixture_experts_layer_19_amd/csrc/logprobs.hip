@@ -255,10 +255,11 @@ __global__ __launch_bounds__(T) void logprob_kernel(LogprobArgs a, int first) {
   };
   if (tid < edges) push(edge(), edge_at);
   __syncthreads();
-  const int owners = s.owners, items = vecs > 0 ? owners * ((vecs + T - 1) / T) : 0;
+  const int owners = s.owners, items = owners * ((vecs + T - 1) / T);
   auto vec_of = [&](int i) MOE_INLINE { return i < items ? i / owners * T + (int)s.owner[i % owners] : vecs; };
   int vec = vec_of(tid);
-  i32x4 u = body[min(vec, vecs - 1)];
+  i32x4 u = {};
+  if (items > 0) u = body[min(vec, vecs - 1)];   // (a row of less than a vector has none)
   for (int i0 = 0; i0 < items; i0 += T) {
     // the next one is on its way while this one's go into the list
     const int next = vec_of(i0 + T + tid);
