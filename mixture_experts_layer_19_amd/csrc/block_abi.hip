@@ -294,7 +294,8 @@ size_t moe_block_linear_workspace_bytes(int32_t rows, int32_t n, int32_t k, int3
   a.rows = rows;
   a.n = n;
   a.k = k;
-  return linear_part_bytes(a) + (codes ? 0 : moe_block_packed_bytes(rows, k) + scale_bytes(rows, k));
+  const bool own = codes || linear_fuses(a);       // no codes are written
+  return linear_part_bytes(a) + (own ? 0 : moe_block_packed_bytes(rows, k) + scale_bytes(rows, k));
 }
 
 moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, int32_t k, const void *x,
@@ -314,6 +315,8 @@ moe_status moe_block_linear(const uint8_t *wq, const float *w_scale, int32_t n, 
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   a.splits = linear_splits(a);
   a.part = (float *)ws;
+  if (!xq && linear_fuses(a))
+    return done(launch_linear_fused(a, x, x_stride, x_dtype == MOE_BF16, out_dtype == MOE_F32, (hipStream_t)stream));
   if (!xq) {
     uint8_t *q = (uint8_t *)ws + linear_part_bytes(a);
     float *scale = (float *)(q + moe_block_packed_bytes(rows, k));

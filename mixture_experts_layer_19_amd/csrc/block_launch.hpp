@@ -101,6 +101,9 @@ hipError_t launch_block_pack(const void *w, long long stride, int src, int n, in
 int linear_splits(const LinearArgs &a);
 size_t linear_part_bytes(const LinearArgs &a);   // workspace of the splits (0: none)
 bool linear_fits(const LinearArgs &a);           // within one launch's workgroups
+bool linear_fuses(const LinearArgs &a);          // whether launch_linear_fused is the one for activations without codes
+hipError_t launch_linear_fused(const LinearArgs &a, const void *x, long long stride, int is_bf16, int f32_out,
+                               hipStream_t stream);
 hipError_t launch_linear(const LinearArgs &a, int f32_out, hipStream_t stream);
 
 // Token log probabilities (logprobs.hip).

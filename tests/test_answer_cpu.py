@@ -104,8 +104,9 @@ def test_sizes(B):
     assert B.moe_block_packed_bytes((1 << 30) + 1, 5) == 0
     assert B.moe_block_packed_bytes(1 << 20, 1 << 20) == 1 << 40
     assert B.moe_block_linear_workspace_bytes(0, 5, 5) == 0
-    assert B.moe_block_linear_workspace_bytes(17, 5, 129) >= 2 * 2 * 2048 + 2 * 32 * 4
-    assert B.moe_block_linear_workspace_bytes(17, 5, 129, codes=True) == 0
+    assert B.moe_block_linear_workspace_bytes(17, 5, 3000) >= 2 * 24 * 2048 + 24 * 32 * 4
+    assert B.moe_block_linear_workspace_bytes(17, 5, 3000, codes=True) == 0
+    assert B.moe_block_linear_workspace_bytes(17, 5, 129) == 0                      # codes in the LDS
     assert B.moe_block_linear_workspace_bytes(70, 100, 8192, codes=True) > 0       # split blocks
 
 
@@ -134,7 +135,7 @@ def test_pack_limits(B):
     refused(B, B.MOE_ERR_UNSUPPORTED, B.moe_block_pack, P, B.MOE_FP8, 1, 1 << 30, 1 << 30, P, None)
 
 
-LINEAR = dict(w=P, ws_=P, n=256, k=512, x=P, xdt=1, xs=512, xq=None, xqs=None, rows=8, out=P, odt=1, ws=P,
+LINEAR = dict(w=P, ws_=P, n=256, k=512, x=P, xdt=1, xs=512, xq=None, xqs=None, rows=100, out=P, odt=1, ws=P,
               size=1 << 30)
 
 
@@ -147,7 +148,7 @@ def test_linear_refuses(B, kw):
 
 
 def test_linear_workspace_and_limits(B):
-    need = B.moe_block_linear_workspace_bytes(8, 256, 512)
+    need = B.moe_block_linear_workspace_bytes(100, 256, 512)
     refused(B, B.MOE_ERR_WORKSPACE, B.moe_block_linear, *{**LINEAR, "size": need - 1}.values())
     refused(B, B.MOE_ERR_WORKSPACE, B.moe_block_linear, *{**LINEAR, "ws": None}.values())
     split = {**LINEAR, "rows": 70, "n": 100, "k": 8192, "x": None, "xs": 0, "xq": P, "xqs": P}
