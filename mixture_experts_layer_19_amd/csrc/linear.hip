@@ -314,8 +314,11 @@ __global__ __launch_bounds__(64 * KW) void block_fused_kernel(LinearArgs a, cons
   const int b0 = (int)((long long)blocks * wave / KW), b1 = (int)((long long)blocks * (wave + 1) / KW);
   const uint8_t *w = a.w + (long long)blockIdx.x * blocks * kBlkBytes + lane * 16;
   const float *ws = a.w_scale + (long long)(blockIdx.x / 8) * blocks;
-  i32x8 wf = {};
-  if (b0 < b1) wf = fragment(w + (long long)b0 * kBlkBytes);       // on its way meanwhile
+  constexpr int AHEAD = 4;                       // blocks of weights on their way, from here on
+  i32x8 wf[AHEAD] = {};
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (b0 < b1) wf[i] = fragment(w + (long long)min(b0 + i, b1 - 1) * kBlkBytes);
 
   // 16 elements a thread, 8 threads a block of a row, two of them on their way at once
   const int units = a.rows * blocks * 8;
@@ -343,20 +346,24 @@ __global__ __launch_bounds__(64 * KW) void block_fused_kernel(LinearArgs a, cons
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b = b0; b < b1; ++b) {
-    const i32x8 next = fragment(w + (long long)min(b + 1, b1 - 1) * kBlkBytes);
-    const float sw = ws[b];
+  for (int b4 = b0; b4 < b1; b4 += AHEAD) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = min(16 * t + (lane & 15), a.rows - 1);
-      const i32x4 *at = (const i32x4 *)(codes + row * pitch + b * kBlk + 32 * (lane >> 4));
-      const i32x8 xf = __builtin_shufflevector(at[0], at[1], 0, 1, 2, 3, 4, 5, 6, 7);
-      const f32x4 p = block_product<F32>(wf, xf);
-      const float s = scales[row * blocks + b] * sw;
+    for (int h = 0; h < AHEAD; ++h) {
+      const int b = b4 + h;
+      if (b >= b1) break;
+      const float sw = ws[b];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], s, acc[t][i]);
+      for (int t = 0; t < RT; ++t) {
+        const int row = min(16 * t + (lane & 15), a.rows - 1);
+        const i32x4 *at = (const i32x4 *)(codes + row * pitch + b * kBlk + 32 * (lane >> 4));
+        const i32x8 xf = __builtin_shufflevector(at[0], at[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const f32x4 p = block_product<F32>(wf[h], xf);
+        const float s = scales[row * blocks + b] * sw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], s, acc[t][i]);
+      }
+      wf[h] = fragment(w + (long long)min(b + AHEAD, b1 - 1) * kBlkBytes);
     }
-    wf = next;
   }
   __syncthreads();
 #pragma unroll
