@@ -125,9 +125,10 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void block_quantize_kernel(const void *x, long long stride, int rows, int cols,
                                                              uint8_t *q, float *scale, int first) {
   const int blocks = (cols + kBlk - 1) / kBlk, rows16 = (rows + 15) / 16 * 16;
-  const long long unit = ((long long)blockIdx.x * 4 + (threadIdx.x >> 6));
-  const int lane = threadIdx.x & 63, b = (int)(unit % blocks), i = lane & 7;
-  const long long row = first + unit / blocks * 8 + (lane >> 3);
+  const uint32_t unit = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t of_rows = unit / (uint32_t)blocks;
+  const int lane = threadIdx.x & 63, b = (int)(unit - of_rows * (uint32_t)blocks), i = lane & 7;
+  const long long row = first + (long long)of_rows * 8 + (lane >> 3);
   if (row >= rows16) return;
   const int k = b * kBlk + 16 * i;
   float v[16];
@@ -600,11 +601,11 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) void block_tile_kern
 template <bool F32>
 __global__ __launch_bounds__(256) void block_join_kernel(LinearArgs a) {
   const int n4 = (a.n + 3) / 4;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, size = (long long)a.rows * n4;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, size = (uint32_t)(a.rows * n4);      // (of at most 512 tiles)
   if (i >= size) return;
-  f32x4 y = *(const f32x4 *)(a.part + 4 * i);
-  for (int s = 1; s < a.splits; ++s) y += *(const f32x4 *)(a.part + 4 * (s * size + i));
-  store4<F32>(a, i / n4, (int)(i % n4) * 4, y);
+  f32x4 y = *(const f32x4 *)(a.part + 4ll * i);
+  for (int s = 1; s < a.splits; ++s) y += *(const f32x4 *)(a.part + 4 * ((long long)s * size + i));
+  store4<F32>(a, i / (uint32_t)n4, (int)(i % (uint32_t)n4) * 4, y);
 }
 
 // ----------------------------------------------------------------------------- launches
