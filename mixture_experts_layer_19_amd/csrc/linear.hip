@@ -120,7 +120,7 @@ __device__ __forceinline__ float largest16(const float (&v)[16]) {
 }
 
 // Activations: a wave takes 8 rows of one block, 8 lanes a row, 16 elements a lane
-// (8192 x 4096 bf16: 23.6 us, 4.3 TB/s).
+// (8192 x 4096 bf16: 20.4 us, 4.9 TB/s).
 template <bool BF16>
 __global__ __launch_bounds__(256) void block_quantize_kernel(const void *x, long long stride, int rows, int cols,
                                                              uint8_t *q, float *scale, int first) {
