@@ -30,7 +30,7 @@ refuses raises :class:`.binding.MoeError`.
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -424,6 +424,7 @@ class BlockCodes(NamedTuple):
     q: torch.Tensor        # packed E4M3 codes, uint8
     scale: torch.Tensor    # float32 [in_features / 128, rows up to a multiple of 16]
     rows: int
+    shape: Tuple[int, int] # (rows, in_features) of what they are the codes of
 
 
 class BlockLinear(_Bound):
@@ -488,7 +489,7 @@ class BlockLinear(_Bound):
         q = torch.empty(B.lib().moe_block_packed_bytes(rows, k), dtype=torch.uint8, device=self.device)
         scale = torch.empty((-(-k // 128), -(-rows // 16) * 16), dtype=torch.float32, device=self.device)
         B.moe_block_quantize(x, self._in, x.stride(0), rows, k, q, scale, _raw_stream(self.device.index))
-        return BlockCodes(q, scale, rows)
+        return BlockCodes(q, scale, rows, (rows, k))
 
     def __call__(self, x: Optional[torch.Tensor] = None, *, codes: Optional[BlockCodes] = None,
                  stream=None) -> torch.Tensor:
@@ -503,6 +504,9 @@ class BlockLinear(_Bound):
             if x is not None:
                 raise ValueError("x and its codes exclude each other")
             rows = codes.rows
+            # (the tensors, filled up to whole blocks, do not tell one width from another)
+            if tuple(codes.shape) != (rows, k):
+                raise ValueError("codes of %s are not those of [%d, %d]" % (list(codes.shape), rows, k))
             want = (-(-k // 128), -(-rows // 16) * 16)
             for t, shape, kind in ((codes.q, (want[0] * want[1] * 128,), torch.uint8),
                                    (codes.scale, want, torch.float32)):

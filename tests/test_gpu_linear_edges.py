@@ -95,3 +95,18 @@ def test_sums_of_bf16_results(act, rows, n, k):
     y = lin(x.cuda())
     check(x, codes, scale, y)
     assert torch.equal(lin(codes=lin.quantize(x.cuda())), y)
+
+
+@pytest.mark.parametrize("rows", [3, 100])
+def test_codes_of_another_size_are_refused(rows):
+    """Sizes that fill the same blocks, which the tensors' shapes do not tell apart."""
+    g = gen(rows)
+    codes, wider = (torch.randn(40, k, generator=g).to(torch.float8_e4m3fn).cuda() for k in (300, 380))
+    scale = torch.ones(1, 3, device="cuda")
+    lin, other = block.BlockLinear(codes, scale), block.BlockLinear(wider, scale)
+    c = lin.quantize(torch.randn(rows, 300, generator=g).to(BF16).cuda())
+    assert lin(codes=c).shape == (rows, 40)
+    for bad in (lambda: other(codes=c), lambda: lin(codes=c._replace(rows=rows + 1)),
+                lambda: lin(codes=c._replace(rows=rows - 1))):
+        with pytest.raises(ValueError):
+            bad()
