@@ -110,3 +110,48 @@ def test_codes_of_another_size_are_refused(rows):
                 lambda: lin(codes=c._replace(rows=rows - 1))):
         with pytest.raises(ValueError):
             bad()
+
+
+# tiles of 128 and of 256 square over many blocks of k, ragged in every size
+LONG = [(1500, 1500, 512), (1409, 1531, 640), (1500, 1500, 2100), (2100, 3904, 512), (2090, 3901, 650),
+        (2100, 3904, 2100)]
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,n,k", LONG)
+def test_large_tiles_over_many_blocks(out, rows, n, k):
+    g = gen(rows + k)
+    x = (torch.randn(rows, k, generator=g) * torch.exp(2 * torch.randn(1, k, generator=g))).to(BF16)
+    codes = (120 * torch.randn(n, k, generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    scale = (0.5 + torch.rand(-(-n // 128), -(-k // 128), generator=g)) / (120 * math.sqrt(k))
+    lin = block.BlockLinear(codes.cuda(), scale.cuda(), out_dtype=out)
+    y = lin(x.cuda())
+    assert torch.equal(lin(codes=lin.quantize(x.cuda())), y)
+    # R.linear_ref's sums, on the device in 64 bits
+    xq, xs = (t.cuda() for t in R.quantize_rows(x))
+    grow = torch.arange(n) // 128
+    want, mag = (torch.zeros(rows, n, dtype=torch.float64, device="cuda") for _ in "ym")
+    for b in range(xs.shape[1]):
+        at = slice(b * 128, (b + 1) * 128)
+        f = xs[:, b:b + 1].double() * scale[grow, b].double().cuda()
+        xb, wb = xq[:, at], codes[:, at].double().T.contiguous().cuda()
+        want += f * torch.mm(xb, wb)
+        mag += f * torch.mm(xb.abs(), wb.abs())
+    bound = R.half_step(out) * want.abs() + (2 * 128 + xs.shape[1] + 4) * R.HALF * mag
+    off = (y.double() - want).abs()
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,n,k", WAYS)
+def test_codes_that_are_nan(out, rows, n, k):
+    """A NaN among the weights' codes, and one that stands beside a zero: their column alone."""
+    codes = torch.ones(n, k).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes[n // 2, k - 1], codes[n - 1, 0] = 0x7F, 0xFF
+    lin = block.BlockLinear(codes.cuda(), torch.ones(-(-n // 128), k // 128, device="cuda"), out_dtype=out)
+    x = torch.ones(rows, k)
+    x[0, 0] = 0.0
+    bad = torch.zeros(n, dtype=torch.bool)
+    bad[[n // 2, n - 1]] = True
+    y = lin(x.to(BF16).cuda()).cpu()
+    assert y[:, bad].isnan().all() and y[:, ~bad].isfinite().all()
