@@ -15,7 +15,7 @@ and behind the block
     residual += x;  logits = norm(residual) Whead;  log p of a token, entropy, the best ones
 
 Projections and logits are products in E4M3 with a scale per block of 128 (or
-torch's).  The second norm writes the activations' 8-bit codes beside the rows, and the
+torch's); base 0 leaves the norms and the turn of heads out.  The second norm writes the activations' 8-bit codes beside the rows, and the
 experts read those.  Weights and inputs are random.
 """
 import argparse
@@ -119,7 +119,7 @@ def main():
     ap.add_argument("--cache", default="mxfp8", choices=("bf16", "mxfp8"))
     ap.add_argument("--experts", default="mxfp8", choices=("bf16", "mxfp8", "w4a8", "fp8"))
     ap.add_argument("--projections", default="fp8", choices=("fp8", "torch"))
-    ap.add_argument("--base", type=float, default=10000.0)
+    ap.add_argument("--base", type=float, default=10000.0, help="of the rotation (0: no norms of heads, no rotation)")
     ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--sinks", type=int, default=0)
     ap.add_argument("--steps", type=int, default=8)
@@ -127,7 +127,7 @@ def main():
     work = dataclasses.replace(inputs.workload("tiny"), H=1024, I=256, Is=256, dtype=a.experts)
     prompts = [611, 7, 64, 255, 1030, 1, 129, 400]
     blk = DecoderBlock(work, heads=16, kv_heads=2, head_dim=64, cache=a.cache, window=a.window, sinks=a.sinks,
-                       projections=a.projections, base=a.base)
+                       projections=a.projections, base=a.base or None)
     table = page_table([n + a.steps for n in prompts], blk.cache.page_size, blk.cache.num_pages)
     g = torch.Generator(device="cuda").manual_seed(1)
 
