@@ -462,10 +462,11 @@ MOE_API moe_status moe_head_norm_rope_write(const moe_head_norm *norm /* host */
  *
  *   y[r][j] = sum_b x_scale[r][b] w_scale[j / 128][b] sum_{c in block b} xq[r][c] wq[j][c]
  *
- * rounded once.  The product of both scales and all sums are fp32.  A block's scale is max|v| times the fp32 number 1/448,
- * rounded to fp32, at least 2^-126, 0 for zeros; its codes are E4M3 of v / scale (the exact
- * quotient, round to nearest even, saturating).  A block with an infinity or NaN gets a NaN scale and NaN codes, which
- * make every sum they enter NaN.
+ * rounded once.  The product of both scales and all sums are fp32.  A block's scale is
+ * max|v| times the fp32 number 1/448 (not max|v| / 448, which may differ by a step), rounded to
+ * fp32, at least 2^-126, 0 for zeros; its codes are E4M3 of v / scale (the exact quotient,
+ * round to nearest even, saturating).  A block with an infinity or NaN gets a NaN scale
+ * and NaN codes, which make every sum they enter NaN.
  *
  * Codes are kept packed: blocks of 16 rows x 128 columns, 2048 bytes,
  * [rows / 16][cols / 128], both counts rounded up and filled with zeros; in a block

@@ -432,7 +432,8 @@ class BlockLinear(_Bound):
     row and 128 columns of x, accumulated in fp32.
 
     weight [out_features, in_features]: float32 or bfloat16, quantised here (a block's
-    scale is max * (1 / 448), both fp32); or E4M3 codes (uint8 or float8_e4m3fn) with their scale
+    scale is max * (1 / 448), both fp32, as x's is: what ``max / 448`` gives on the GPU, which may
+    differ by a step from the quotient); or E4M3 codes (uint8 or float8_e4m3fn) with their scale
     [out_features / 128, in_features / 128] float32, rounded up.  Either is packed
     once; codes of quantised weights are not kept otherwise.  dtype: x's, float32 or bfloat16; out_dtype:
     y's, dtype if not given.  Any sizes."""

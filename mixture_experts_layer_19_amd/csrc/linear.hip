@@ -47,7 +47,9 @@ __device__ __forceinline__ i32x8 fragment(const uint8_t *p) {
 
 // Scale of a block with the largest magnitude am: am times the fp32 number 1/448, rounded
 // to fp32, 0 for zeros, at least the smallest normal number otherwise; NaN for an infinity
-// or NaN.
+// or NaN.  Not am / 448, which differs by a step for some am: this is what torch on the GPU
+// makes of a division by the constant 448, so that activations quantised with it have the
+// same scales and codes.
 __device__ __forceinline__ float block_scale(float am) {
   return am > 0.0f && am < INFINITY ? fmaxf(am * (1.0f / 448.0f), 0x1p-126f) : am == 0.0f ? 0.0f : __builtin_nanf("");
 }
